@@ -11,3 +11,5 @@ from . import model  # noqa: F401
 from .model import GPT, GPTConfig, PRESETS, preset  # noqa: F401
 from . import optim  # noqa: F401
 from .optim import AdamW, MuonAdamW, lr_schedule  # noqa: F401
+from . import kv  # noqa: F401
+from .kv import KVBatch, KVCache  # noqa: F401

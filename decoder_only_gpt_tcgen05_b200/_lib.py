@@ -59,6 +59,12 @@ SIGNATURES = {
     "gpt_grad_buckets": [_P, C.c_int32, _P, _P, _P],
     "gpt_backward_bucketed": [_P, _P, _I, _I, _P, C.c_size_t, _P, _I, _P, _I, _P],
     "gpt_muon_step": [_P, _P, _P, _P, _P, _LL, _P, _P, _P],
+    "gpt_kv_tile_bytes": [_I, _I, _P],
+    "gpt_op_kv_append": [_P, _P, _P, _I, _I, _I, _I, _F, _F, _P, _P],
+    "gpt_op_kv_read": [_P, _P, _I, _P, _P, _P],
+    "gpt_op_kv_select": [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P],
+    "gpt_op_attention_kv_scratch_size": [_P, _P, _I, _I, _I, _P],
+    "gpt_op_attention_kv": [_P, _P, _P, _I, _I, _I, _P, _I, _P, _P, _P, C.c_size_t, _P],
 }
 
 
@@ -73,6 +79,18 @@ class AdamWParams(C.Structure):
     """gpt_adamw of include/gpt.h."""
     _fields_ = [("lr", C.c_float), ("beta1", C.c_float), ("beta2", C.c_float), ("eps", C.c_float),
                 ("weight_decay", C.c_float), ("grad_scale", C.c_float), ("grad_clip", C.c_float)]
+
+
+class KVCacheParams(C.Structure):
+    """gpt_kv_cache of include/gpt_ops.h."""
+    _fields_ = [("tiles", C.c_void_p), ("bounds", C.c_void_p), ("n_blocks", C.c_int32), ("n_kv_head", C.c_int32),
+                ("head_dim", C.c_int32), ("bits", C.c_int32)]
+
+
+class KVBatchParams(C.Structure):
+    """gpt_kv_batch of include/gpt_ops.h."""
+    _fields_ = [("block_table", C.c_void_p), ("lens", C.c_void_p), ("cu_new", C.c_void_p), ("n_seq", C.c_int32),
+                ("max_blocks", C.c_int32), ("max_new", C.c_int32)]
 
 
 def lib():

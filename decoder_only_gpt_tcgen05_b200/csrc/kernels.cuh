@@ -14,7 +14,7 @@
 
 namespace gptk {
 
-enum : unsigned int { DEV_ERR_BAD_TOKEN = 2u };
+enum : unsigned int { DEV_ERR_BAD_TOKEN = 2u, DEV_ERR_BAD_BATCH = 3u };
 
 // fp32 -> bf16, n elements (n % 4 == 0, 16-byte aligned)
 int launch_cast_bf16(const float* src, __nv_bfloat16* dst, long long n, cudaStream_t st);

@@ -1029,6 +1029,9 @@ GPT_API int gpt_sync_status(void* stream) {
     return set_error(ST_DEVICE_TIMEOUT, "a kernel gave up a bounded wait (site " + std::to_string(site) + ", block " +
                                             std::to_string(blk) + ")");
   if (code == DEV_ERR_BAD_TOKEN) return set_error(ST_INVALID_ARG, "a token id was outside [0, vocab_size)");
+  if (code == DEV_ERR_BAD_BATCH)
+    return set_error(ST_INVALID_ARG, "a cached batch had a block number, length or row range outside its limits (site " +
+                                         std::to_string(site) + ")");
   return set_error(ST_CUDA, "device status word " + std::to_string(v));
 }
 

@@ -1,0 +1,170 @@
+"""The quantised key/value cache of one attention layer (include/gpt_ops.h: gpt_kv_cache and the
+calls that take it) on torch tensors.
+
+``KVCache`` bundles a layer's cache buffers; ``KVBatch`` describes the sequences of a call and their
+new tokens and is shared by all layers.  A step of a layer is ``append`` (RoPE, QK-norm, quantise),
+then ``attend``, over everything or over the blocks that ``select`` chose.  Nothing is read back to
+the host, so a step can be captured into a CUDA graph and replayed with new contents."""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+
+import torch
+
+from ._lib import KVBatchParams, KVCacheParams, call
+
+KV_BLOCK = 64  # tokens of a cache block
+
+
+def tile_bytes(bits: int, head_dim: int) -> int:
+    """Bytes of one block and kv head: codes and scales of 64 keys and 64 values."""
+    n = C.c_size_t()
+    call("gpt_kv_tile_bytes", bits, head_dim, C.byref(n))
+    return n.value
+
+
+def _on(dev: torch.device):
+    """Launches go to the tensors' device, whichever is current."""
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _stream(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _check(t: torch.Tensor, name: str, dtype, dev, shape=None) -> None:
+    assert t.dtype == dtype, f"{name}: {dtype} needed, got {t.dtype}"
+    assert t.device == dev, f"{name}: on {t.device}, the cache is on {dev}"
+    assert t.is_contiguous(), f"{name}: must be contiguous"
+    assert shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} needed, got {tuple(t.shape)}"
+
+
+class KVBatch:
+    """Sequences and their new tokens (gpt_kv_batch): ``block_table`` int32 [n_seq, max_blocks], ``lens``
+    int32 [n_seq] (new tokens included) and ``cu_new`` int32 [n_seq + 1], the first row of each
+    sequence in the row tensors (None: one new token each, row b for sequence b); ``max_new``: the most
+    new tokens a sequence has.  The tensors are kept, not copied: update them in place between steps."""
+
+    def __init__(self, block_table: torch.Tensor, lens: torch.Tensor, cu_new: torch.Tensor | None = None, *,
+                 max_new: int = 1):
+        dev = block_table.device
+        assert block_table.dim() == 2, "block_table: [n_seq, max_blocks]"
+        n, w = block_table.shape
+        _check(block_table, "block_table", torch.int32, dev)
+        _check(lens, "lens", torch.int32, dev, (n,))
+        if cu_new is not None:
+            _check(cu_new, "cu_new", torch.int32, dev, (n + 1,))
+        assert max_new >= 0 and (cu_new is not None or max_new == 1), "max_new: without cu_new it is 1"
+        self.block_table, self.lens, self.cu_new, self.max_new, self.device = block_table, lens, cu_new, max_new, dev
+        self.n_seq = n
+        self._c = KVBatchParams(block_table.data_ptr(), lens.data_ptr(), cu_new.data_ptr() if cu_new is not None else None,
+                                n, w, max_new)
+        self._ref = C.byref(self._c)
+
+
+class KVCache:
+    """The cache of one attention layer: ``n_blocks`` blocks of 64 tokens for ``n_kv_head`` heads of
+    ``head_dim`` (64 or 128) in ``bits`` (4 or 8).  ``bounds``: keep the elementwise key bounds of each
+    block that ``select`` needs.  ``tiles`` and ``bounds`` may be given as tensors made earlier."""
+
+    def __init__(self, n_blocks: int, n_kv_head: int, head_dim: int, *, bits: int = 8, device="cuda:0",
+                 tiles: torch.Tensor | None = None, bounds: torch.Tensor | bool = True):
+        tb = tile_bytes(bits, head_dim)
+        dev = tiles.device if tiles is not None else torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        if tiles is None:
+            tiles = torch.zeros((n_blocks, n_kv_head, tb), dtype=torch.uint8, device=dev)
+        _check(tiles, "tiles", torch.uint8, dev, (n_blocks, n_kv_head, tb))
+        if bounds is True:
+            bounds = torch.zeros((n_blocks, n_kv_head, 2, head_dim), dtype=torch.bfloat16, device=dev)
+        elif bounds is False:
+            bounds = None
+        if bounds is not None:
+            _check(bounds, "bounds", torch.bfloat16, dev, (n_blocks, n_kv_head, 2, head_dim))
+        self.n_blocks, self.n_kv_head, self.head_dim, self.bits = n_blocks, n_kv_head, head_dim, bits
+        self.tiles, self.bounds, self.device = tiles, bounds, dev
+        self._c = KVCacheParams(tiles.data_ptr(), bounds.data_ptr() if bounds is not None else None, n_blocks,
+                                n_kv_head, head_dim, bits)
+        self._ref = C.byref(self._c)
+
+    def append(self, batch: KVBatch, qkv: torch.Tensor, n_head: int, *, rope: bool = True, qk_norm: bool = True,
+               rope_base: float = 10000.0, eps: float = 1e-5, q: torch.Tensor | None = None) -> torch.Tensor:
+        """Writes the new tokens' keys and values (``qkv``: bf16 [M, (n_head + 2 n_kv_head) head_dim], raw)
+        and returns their queries after RoPE and QK-norm, bf16 [M, n_head head_dim]."""
+        M = qkv.shape[0]
+        _check(qkv, "qkv", torch.bfloat16, self.device, (M, (n_head + 2 * self.n_kv_head) * self.head_dim))
+        assert batch.device == self.device, "batch: on another device than the cache"
+        if q is None:
+            q = torch.empty((M, n_head * self.head_dim), dtype=torch.bfloat16, device=self.device)
+        _check(q, "q", torch.bfloat16, self.device, (M, n_head * self.head_dim))
+        with _on(self.device):
+            call("gpt_op_kv_append", self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope), int(qk_norm),
+                 rope_base, eps, q.data_ptr(), _stream(self.device))
+        return q
+
+    def read(self, batch: KVBatch, M: int, *, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+        """(k, v): bf16 [M, n_kv_head, head_dim], the values cached at the batch's new positions."""
+        shape = (M, self.n_kv_head, self.head_dim)
+        assert batch.device == self.device, "batch: on another device than the cache"
+        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
+        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
+        _check(k, "k", torch.bfloat16, self.device, shape)
+        _check(v, "v", torch.bfloat16, self.device, shape)
+        with _on(self.device):
+            call("gpt_op_kv_read", self._ref, batch._ref, M, k.data_ptr(), v.data_ptr(), _stream(self.device))
+        return k, v
+
+    def _heads(self, q: torch.Tensor) -> int:
+        assert q.dim() == 2 and q.shape[1] % self.head_dim == 0, "q: [M, n_head head_dim]"
+        return q.shape[1] // self.head_dim
+
+    def select(self, batch: KVBatch, q: torch.Tensor, n_select: int, *, n_first: int = 1, n_last: int = 1,
+               blocks: torch.Tensor | None = None, scores: torch.Tensor | None = None):
+        """(blocks int32 [M, n_kv_head, n_select], scores fp32 [M, n_kv_head, max_blocks]): the blocks each
+        new token attends to, by the bound of their keys' scores; the first ``n_first`` and last ``n_last``
+        visible ones always."""
+        M, H = q.shape[0], self._heads(q)
+        _check(q, "q", torch.bfloat16, self.device)
+        assert batch.device == self.device, "batch: on another device than the cache"
+        shapes = (M, self.n_kv_head, n_select), (M, self.n_kv_head, batch.block_table.shape[1])
+        blocks = torch.empty(shapes[0], dtype=torch.int32, device=self.device) if blocks is None else blocks
+        scores = torch.empty(shapes[1], dtype=torch.float32, device=self.device) if scores is None else scores
+        _check(blocks, "blocks", torch.int32, self.device, shapes[0])
+        _check(scores, "scores", torch.float32, self.device, shapes[1])
+        with _on(self.device):
+            call("gpt_op_kv_select", self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
+                 blocks.data_ptr(), scores.data_ptr(), _stream(self.device))
+        return blocks, scores
+
+    def scratch_bytes(self, batch: KVBatch, M: int, n_head: int, n_sel: int = 0) -> int:
+        n = C.c_size_t()
+        call("gpt_op_attention_kv_scratch_size", self._ref, batch._ref, M, n_head, n_sel, C.byref(n))
+        return n.value
+
+    def attend(self, batch: KVBatch, q: torch.Tensor, *, window: int = -1, blocks: torch.Tensor | None = None,
+               o: torch.Tensor | None = None, lse: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
+        """(o bf16 [M, n_head head_dim], lse fp32 [M, n_head]): attention of the new tokens over the cache,
+        over all earlier keys, over the last ``window`` and itself, or over the listed ``blocks``.
+        ``scratch`` (uint8, scratch_bytes) may be passed in; calls that overlap need their own."""
+        M, H = q.shape[0], self._heads(q)
+        _check(q, "q", torch.bfloat16, self.device)
+        assert batch.device == self.device, "batch: on another device than the cache"
+        n_sel = 0
+        if blocks is not None:
+            n_sel = blocks.shape[-1]
+            _check(blocks, "blocks", torch.int32, self.device, (M, self.n_kv_head, n_sel))
+            assert n_sel > 0, "blocks: at least one entry a list"
+        o = torch.empty_like(q) if o is None else o
+        lse = torch.empty((M, H), dtype=torch.float32, device=self.device) if lse is None else lse
+        _check(o, "o", torch.bfloat16, self.device, (M, H * self.head_dim))
+        _check(lse, "lse", torch.float32, self.device, (M, H))
+        if scratch is None:
+            scratch = torch.empty(self.scratch_bytes(batch, M, H, n_sel), dtype=torch.uint8, device=self.device)
+        _check(scratch, "scratch", torch.uint8, self.device)
+        with _on(self.device):
+            call("gpt_op_attention_kv", self._ref, batch._ref, q.data_ptr(), M, H, int(window),
+                 blocks.data_ptr() if blocks is not None else None, n_sel, o.data_ptr(), lse.data_ptr(),
+                 scratch.data_ptr(), scratch.numel(), _stream(self.device))
+        return o, lse

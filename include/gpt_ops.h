@@ -188,6 +188,122 @@ GPT_API int gpt_op_adamw(float* params, const float* grads, float* m, float* v, 
                          const int64_t* run_start, const uint8_t* run_decay, int32_t n_runs, int64_t step,
                          const gpt_adamw* h, void* scratch, double* grad_norm, void* stream);
 
+/* ---- Quantised key/value cache: append, read back, attend, select blocks.
+ *
+ * Answering with a model reads the keys and values of every earlier token
+ * again for each new one ("Train your own ChatGPT", read the source
+ * engine.py: the KV cache).  These calls keep them in 4 or 8 bits, in blocks
+ * of GPT_KV_BLOCK tokens that sequences hold through block tables.
+ *
+ * A cache block holds, for each kv head, one tile of gpt_kv_tile_bytes bytes:
+ * two records of 32 tokens, each
+ *   [32 key rows][32 value rows][32 x NG key scales][32 x NG value scales]
+ * with unsigned codes, bf16 scales and value = scale (code - Z); Z = 8 and one
+ * scale per 64 dims (4 bits), Z = 128 and one scale per row (8 bits).  With
+ * R = head_dim bits / 8 bytes of a row in natural order (dim 0 first, the low
+ * nibble the even dim), byte y of token i lies, within its record, at
+ *   keys:   w = y / 4, x = 4 (w / 4) + y % 4, P = min(R / 4, 16):
+ *           (i / 16) 16 R + (x / P) 64 P + (i % 16) 4 P + (w % 4) P + x % P
+ *   values: o = y / bits (8 dims), n = i % 16,
+ *           z = (n % 2 + 2 (n / 8)) R / 8 + (o / 8) bits + y % bits:
+ *           32 R + (i / 16) 16 R + (z / 16) 512 + (4 (o % 8) + n % 8 / 2) 16 + z % 16
+ * (the order in which the attention kernel's operands take them). */
+#define GPT_KV_BLOCK 64
+
+typedef struct gpt_kv_cache {
+  void* tiles;        /* device [n_blocks, n_kv_head, tile bytes], 16-byte aligned                  */
+  void* bounds;       /* device bf16 [n_blocks, n_kv_head, 2, head_dim]: elementwise minimum and
+                         maximum of a block's keys, 16-byte aligned; NULL: not kept                 */
+  int32_t n_blocks;
+  int32_t n_kv_head;
+  int32_t head_dim;   /* 64 or 128                                                                  */
+  int32_t bits;       /* 4 or 8                                                                     */
+} gpt_kv_cache;
+
+/* A ragged batch of sequences with new tokens.  Row tensors (qkv, q, o, ...)
+ * hold the new tokens of sequence b in rows cu_new[b] .. cu_new[b + 1] - 1,
+ * oldest first; its last row is the token at position lens[b] - 1.  Rows that
+ * belong to no sequence are left as they are.  The three arrays are DEVICE
+ * memory: nothing is copied to the host, so their contents may change between
+ * replays of a captured graph.
+ *
+ * A sequence must have 0 <= new tokens <= max_new, lens[b] >= its new tokens,
+ * lens[b] <= 64 max_blocks and rows within [0, M); one that has not is left
+ * out of the call.  cu_new must not decrease; a row that two sequences claim
+ * holds the result of either.  A block number outside [0, n_blocks) that a call would use
+ * is never followed: append skips those tokens, read and attention give NaN.
+ * Both are reported by gpt_sync_status (GPT_ERR_INVALID_ARG). */
+typedef struct gpt_kv_batch {
+  const int32_t* block_table;  /* [n_seq, max_blocks] cache block of each 64 tokens, in order        */
+  const int32_t* lens;         /* [n_seq] tokens of each sequence, the new ones included             */
+  const int32_t* cu_new;       /* [n_seq + 1] first row of each sequence; NULL: row b is sequence b's */
+  int32_t n_seq;
+  int32_t max_blocks;
+  int32_t max_new;             /* most new tokens a sequence has (ignored without cu_new)            */
+} gpt_kv_batch;
+
+GPT_API int gpt_kv_tile_bytes(int bits, int head_dim, size_t* bytes);
+
+/* Appends the new tokens' keys and values to the cache and gives their
+ * queries: the first stage of gpt_op_attention_fwd (RoPE at the token's
+ * position, then per-head RMSNorm of q and k), for a cache.
+ *   qkv    bf16 [M, (H + 2 n_kv_head) hd]: q heads, then k heads, then v heads
+ *   q_out  bf16 [M, H hd]: q after RoPE (if rope) and RMSNorm (if qk_norm)
+ * Per scale group, with top = 7 or 127: scale = bf16(max|x| / top),
+ * code - Z = round(x / scale) clamped to [-top, top] (k is not rounded to bf16
+ * in between).  A group that holds an infinity or a NaN reads back as NaN; one
+ * whose scale would be below 2^-126, as zeros.  Angles are formed in fp64.
+ * With bounds, those of every touched block become the outward rounded
+ * elementwise minimum and maximum of the values its keys now stand for; a
+ * block whose first token is among the new ones starts afresh, otherwise the
+ * new keys widen what was there (so writing a position again may leave them
+ * wider than need be, never narrower).
+ * Two sequences of one call must not write to the same block. */
+GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batch, const void* qkv, int M, int H,
+                             int rope, int qk_norm, float rope_base, float eps, void* q_out, void* stream);
+
+/* Reads the cached keys and values at the batch's new positions back as bf16
+ * rows [M, n_kv_head, hd] (for a whole sequence: as many new tokens as
+ * lens[b]). */
+GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch, int M, void* k_out, void* v_out,
+                           void* stream);
+
+/* Scores the cache blocks each new token can see and chooses n_select of them.
+ *   score_j = sum over the kv head's H / n_kv_head query heads and the dims d
+ *             of max(q_d min_jd, q_d max_jd)
+ * (no key of block j can give more), summed in fp64 and rounded to fp32.
+ * Chosen are the first n_first and the last n_last visible blocks, then those
+ * with the highest scores, equal ones by the lower index (a NaN score is
+ * chosen before any other).
+ *   blocks int32 [M, n_kv_head, n_select] out: indices into the sequence's
+ *          block table, ascending; -1 after the last when fewer are visible
+ *   scores fp32 [M, n_kv_head, max_blocks] out: -inf for blocks not visible
+ * n_first + n_last <= n_select; H / n_kv_head <= 32; the cache keeps bounds. */
+GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batch, const void* q, int M, int H,
+                             int n_select, int n_first, int n_last, int32_t* blocks, float* scores, void* stream);
+
+/* Attention of the new tokens over the cache (their own keys included: append
+ * first): o = softmax(q k^T / sqrt(hd) + mask) v, for a token at position p
+ * over the keys at 0 .. p, with window >= 0 over p - window .. p, and with
+ * sel over the listed blocks' keys at 0 .. p.  Query head i uses kv head
+ * i / (H / n_kv_head).
+ *   q    bf16 [M, H hd], as gpt_op_kv_append gives it
+ *   sel  int32 [M, n_kv_head, n_sel] block-table indices, or NULL with
+ *        n_sel = 0; of each list the first min(n_sel, visible blocks) entries
+ *        are read, those negative or not visible are passed over, and a block
+ *        listed twice counts twice.  Takes no window (-1).
+ *   o    bf16 [M, H hd]; lse fp32 [M, H], natural-log logsumexp of the scores
+ *        (may be NULL).  A row without keys gets o = 0 and lse = -inf.
+ *   scratch  gpt_op_attention_kv_scratch_size bytes, 256-byte aligned; calls
+ *        that may overlap need scratch of their own
+ * Results do not depend on timing, but the split of the keys (and with it the
+ * last bits) depends on the whole batch. */
+GPT_API int gpt_op_attention_kv_scratch_size(const gpt_kv_cache* cache, const gpt_kv_batch* batch, int M, int H,
+                                             int n_sel, size_t* bytes);
+GPT_API int gpt_op_attention_kv(const gpt_kv_cache* cache, const gpt_kv_batch* batch, const void* q, int M, int H,
+                                int window, const int32_t* sel, int n_sel, void* o, float* lse, void* scratch,
+                                size_t scratch_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -8,3 +8,4 @@ from .gpt_oracle import Config  # noqa: F401
 from .presets import PRESETS, preset  # noqa: F401
 from . import optim_oracle as optim  # noqa: F401,E402
 from . import fp8_oracle as fp8  # noqa: F401,E402
+from . import kv_oracle as kv  # noqa: F401,E402

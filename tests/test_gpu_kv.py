@@ -1,0 +1,734 @@
+"""The quantised key/value cache on the GPU against the float64 oracle (oracle/kv_oracle.py).
+
+Tolerances, from the roundings the kernels make:
+  - q after RoPE and QK-norm: half a bf16 step, 2^-8 |q|, plus fp32 arithmetic: 16 operations of
+    2^-24 on terms up to the row's largest raw value times its norm factor, 2^-20 of the row's largest.
+  - cached values: half a step of the quantiser, half a bf16 step for the value read back, and the
+    fp32 error above; and equal to the oracle's own value wherever the quotient is not within 2^-12
+    of a border between two codes (the scale itself may sit on a border: those groups are let off).
+  - attention: the probabilities times the value scale are fp16 operands, off by 2^-11 of themselves
+    (and by 2^-25 / 64 of the largest value scale's power of two, absolutely), so a row by
+    2^-11 sum_j p_j |v_j|; the scores are fp32 sums of exact products of q and codes, off by at most
+    e_s = 2^-20 sum_d |q_d| 2 Z scale / sqrt(hd), which moves each p_j by 2 e_s of itself; the
+    accumulated sums hold p scale (code - Z) as differences of terms up to p scale 2 Z, 2^-20 of
+    those; and the output is bf16, 2^-8 |o|.  lse: e_s + 2^-21 (1 + |lse|).
+  - block scores: fp64 sums rounded to fp32, 2^-24; chosen blocks: equal."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import synth
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+
+
+def _g():
+    import decoder_only_gpt_tcgen05_b200 as g
+    return g
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
+
+
+def normal(shape, seed):
+    return synth.normal(shape, seed).astype(np.float64)
+
+
+def bf(x):
+    return torch.from_numpy(np.asarray(x, np.float32)).bfloat16().to(DEV)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+class World:
+    """A cache with random contents: sequences of the given lengths in shuffled blocks; every byte that
+    holds no token (slots after a sequence's end, unused blocks) is 0xff, a NaN scale."""
+
+    def __init__(self, bits, hd, Hkv, lens, seed, scale=1.0, spare=3):
+        self.bits, self.hd, self.Hkv, self.lens = bits, hd, Hkv, list(lens)
+        g = _g()
+        need = [(n + 63) // 64 for n in lens]
+        self.W = max(need + [1]) + 1
+        self.n_blocks = sum(need) + spare
+        perm = np.random.default_rng(seed).permutation(self.n_blocks)
+        self.table = np.full((len(lens), self.W), -7)
+        at = 0
+        for b, n in enumerate(need):
+            self.table[b, :n] = perm[at:at + n]
+            at += n
+        tile = 2 * O.kv.geometry(bits, hd)[2]
+        tiles = np.full((self.n_blocks, Hkv, tile), 255, np.uint8)
+        bounds = np.full((self.n_blocks, Hkv, 2, hd), np.nan)
+        self.k, self.v = [], []
+        R, ng, recb = O.kv.geometry(bits, hd)
+        tabs = O.kv._tables(bits, hd)
+        for b, n in enumerate(lens):
+            x = normal((2, n, Hkv, hd), seed + 17 * b + 1) * scale
+            parts = [O.kv.quantise(x[i], bits) for i in range(2)]
+            self.k.append(parts[0][2])
+            self.v.append(parts[1][2])
+            for j in range(need[b]):
+                m = min(64, n - 64 * j)
+                for i in range(m):
+                    rec, tok = divmod(i, 32)
+                    dst = tiles[self.table[b, j], :, rec * recb:(rec + 1) * recb]
+                    for which in range(2):
+                        c, s = (p[64 * j + i] for p in parts[which][:2])
+                        dst[:, tabs[which][tok]] = c if bits == 8 else c[:, 0::2] | (c[:, 1::2] << 4)
+                        raw = (s.astype(np.float32).view(np.uint32) >> 16).astype(np.uint16).reshape(Hkv, ng, 1)
+                        so = 2 * 32 * R + which * 64 * ng + tok * 2 * ng
+                        dst[:, so:so + 2 * ng] = raw.view(np.uint8).reshape(Hkv, 2 * ng)
+                kk = self.k[b][64 * j:64 * j + m]
+                bounds[self.table[b, j]] = np.stack((O.kv.bf16(kk.min(0), "down"), O.kv.bf16(kk.max(0), "up")), 1)
+        self.bounds = bounds
+        self.cache = g.KVCache(self.n_blocks, Hkv, hd, bits=bits, tiles=torch.from_numpy(tiles).to(DEV), bounds=bf(bounds))
+
+    def batch(self, new, max_new=None):
+        cu = np.concatenate(([0], np.cumsum(new)))
+        b = _g().KVBatch(i32(self.table), i32(self.lens), i32(cu), max_new=max(new) if max_new is None else max_new)
+        return b, cu
+
+
+def attend_bounds(w, b, q, o, lse, av, weight):
+    """The tolerances of one token's row (module docstring): (of o [H, hd], of lse [H])."""
+    G = q.shape[0] // w.Hkv
+    Z = 1 << (w.bits - 1)
+    to, tl = np.zeros_like(o), np.zeros(len(lse))
+    for h in range(q.shape[0]):
+        live = weight[h // G] > 0
+        if not live.any():
+            continue
+        ksc = np.abs(w.k[b][live, h // G]).max() / (Z - 1) * 1.01
+        vsc = np.abs(w.v[b][live, h // G]).max() / (Z - 1) * 1.01
+        es = 2.0 ** -20 * np.abs(q[h]).sum() * 2 * Z * ksc / np.sqrt(w.hd)
+        n = weight[h // G].sum()
+        to[h] = 2.0 ** -8 * np.abs(o[h]) + (2.0 ** -11 + 2 * es) * av[h] + 2.0 ** -20 * 2 * Z * vsc + \
+            n * 2.0 ** -31 * 2 * vsc * Z * np.exp(-min(0.0, lse[h]))
+        tl[h] = es + 2.0 ** -21 * (1 + abs(lse[h]))
+    return to, tl
+
+
+def check_attend(w, new, q, o, lse, window=-1, sel=None, what=""):
+    """Every row of o, lse against the oracle; sel: [M, Hkv, n] listed blocks."""
+    cu = np.concatenate(([0], np.cumsum(new)))
+    H = q.shape[1] // w.hd
+    for b, n in enumerate(new):
+        for i in range(n):
+            m, p = cu[b] + i, w.lens[b] - n + i
+            L = w.lens[b]
+            j = np.arange(L)
+            ok = (j <= p) & ((j >= p - window) if window >= 0 else True)
+            wt = np.repeat(ok[None].astype(float), w.Hkv, 0)
+            if sel is not None:
+                nb = p // 64 + 1
+                for h in range(w.Hkv):
+                    cnt = np.zeros(w.W + 1)
+                    for x in sel[m, h][:min(sel.shape[2], nb)]:
+                        if 0 <= x < nb:
+                            cnt[x] += 1
+                    wt[h] *= cnt[j // 64]
+            qr = q[m].reshape(H, w.hd)
+            ro, rl, av = O.kv.attend(qr, w.k[b], w.v[b], wt)
+            to, tl = attend_bounds(w, b, qr, ro, rl, av, wt)
+            got = o[m].reshape(H, w.hd)
+            assert np.all(np.isfinite(got)), (what, b, i)
+            assert np.all(np.abs(got - ro) <= to), (what, b, i, (np.abs(got - ro) - to).max(), np.abs(ro).max())
+            dead = ~np.isfinite(rl)
+            assert np.all(lse[m][dead] == -np.inf) and np.all(got[dead] == 0), (what, b, i)
+            assert np.all(np.abs(lse[m] - rl)[~dead] <= tl[~dead]), (what, b, i, np.abs(lse[m] - rl)[~dead].max())
+
+
+# ---------------------------------------------------------------------------- append and read
+
+APPEND = [
+    # bits, hd, H, Hkv, rope, norm, lens, new tokens
+    (8, 128, 2, 2, True, True, [1, 64, 65, 200], [1, 1, 1, 1]),
+    (4, 128, 2, 2, True, True, [1, 64, 65, 200], [1, 1, 1, 1]),
+    (4, 128, 4, 2, True, True, [130, 64, 5, 131], [130, 63, 0, 66]),
+    (8, 64, 4, 1, True, True, [130, 64, 5, 131], [130, 63, 0, 66]),
+    (4, 64, 3, 3, False, True, [7, 100], [3, 2]),
+    (8, 128, 6, 3, True, False, [77, 129], [8, 9]),
+    (8, 64, 12, 12, False, False, [300], [300]),
+    (4, 128, 10, 10, True, True, [1000], [333]),
+]
+
+
+@pytest.mark.parametrize("case", APPEND)
+def test_append_and_read_match_the_oracle(case):
+    bits, hd, H, Hkv, rope, norm, lens, new = case
+    w = World(bits, hd, Hkv, [n - m for n, m in zip(lens, new)], 100)
+    # the sequences grow into spare blocks
+    need = [(n + 63) // 64 for n in lens]
+    had = [(n - m + 63) // 64 for n, m in zip(lens, new)]
+    grow = sum(need) - sum(had)
+    g = _g()
+    cache = g.KVCache(w.n_blocks + grow, Hkv, hd, bits=bits, device=DEV)
+    cache.tiles.fill_(255)
+    cache.bounds.fill_(float("nan"))
+    cache.tiles[:w.n_blocks] = w.cache.tiles
+    cache.bounds[:w.n_blocks] = w.cache.bounds
+    table = np.full((len(lens), max(need) + 2), -1)
+    fresh = w.n_blocks
+    for b in range(len(lens)):
+        table[b, :had[b]] = w.table[b, :had[b]]
+        for j in range(had[b], need[b]):
+            table[b, j] = fresh
+            fresh += 1
+    before_t, before_b = cache.tiles.clone(), cache.bounds.clone()
+    M, behind = sum(new), 3
+    cu = np.concatenate(([0], np.cumsum(new)))
+    raw = torch.from_numpy(synth.normal((M + behind, (H + 2 * Hkv) * hd), 5)).bfloat16()
+    batch = g.KVBatch(i32(table), i32(lens), i32(cu), max_new=max(new))
+    q = torch.full((M + behind, H * hd), 7.0, dtype=torch.bfloat16, device=DEV)
+    cache.append(batch, raw.to(DEV), H, rope=rope, qk_norm=norm, q=q)
+    k = torch.full((M + behind, Hkv, hd), 7.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    cache.read(batch, M + behind, k=k, v=v)
+    g.model.sync_status(DEV)
+    for t in (q, k, v):
+        assert torch.all(t[M:] == 7.0)          # rows behind the last sequence
+    q, k, v = f64(q), f64(k), f64(v)
+    phi = O.rope_angles(max(lens), hd, 10000.0)
+    used = {}
+    for b, n in enumerate(new):
+        if n == 0:
+            continue
+        x = raw[cu[b]:cu[b + 1]].double().numpy().reshape(n, H + 2 * Hkv, hd)
+        pos = np.arange(lens[b] - n, lens[b])
+        y = x[:, :H + Hkv]
+        if rope:
+            y = O.rope(y.transpose(1, 0, 2), phi[pos]).transpose(1, 0, 2)
+        f = np.ones(y.shape[:2] + (1,))
+        if norm:
+            y, f = O.rmsnorm(y, 1e-5)
+            f = f.reshape(*y.shape[:2], 1)
+        top = np.abs(x[:, :H + Hkv]).max(-1, keepdims=True) * np.abs(f)
+        eq = 2.0 ** -8 * np.abs(y) + 2.0 ** -20 * top
+        assert np.all(np.abs(q[cu[b]:cu[b + 1]].reshape(n, H, hd) - y[:, :H]) <= eq[:, :H])
+        for got, ref, err in ((k[cu[b]:cu[b + 1]], y[:, H:], 2.0 ** -20 * top[:, H:]),
+                              (v[cu[b]:cu[b + 1]], x[:, H + Hkv:], 0.0)):
+            _, s, val = O.kv.quantise(ref, bits)
+            step = np.repeat(s, hd // s.shape[-1], -1)
+            assert np.all(np.abs(got - ref) <= 0.5 * step * (1 + 2.0 ** -7) + 2.0 ** -8 * np.abs(got) + err)
+            quo = ref / step
+            clear = np.abs(quo - np.floor(quo) - 0.5) > 2.0 ** -12
+            amax = np.abs(ref.reshape(n, Hkv, s.shape[-1], -1)).max(-1) / ((1 << (bits - 1)) - 1)
+            edge = O.kv.bf16(amax * (1 - 2.0 ** -19)) != O.kv.bf16(amax * (1 + 2.0 ** -19))
+            clear &= ~np.repeat(edge, hd // s.shape[-1], -1)
+            assert np.all(np.abs(got - val)[clear] <= 2.0 ** -8 * np.abs(val)[clear]) and clear.mean() > 0.9
+        for j in range((lens[b] - n) // 64, (lens[b] + 63) // 64):
+            used[table[b, j]] = (b, j, max(lens[b] - n - 64 * j, 0), min(lens[b] - 64 * j, 64))
+    # what was in the cache stays, but for the slots written; bounds hold every key of the block
+    kk, vv = (O.kv.unpack(cache.tiles.cpu().numpy(), bits, hd))
+    k0, v0 = O.kv.unpack(before_t.cpu().numpy(), bits, hd)
+    bd, bd0 = f64(cache.bounds), f64(before_b)
+    for ph in range(cache.n_blocks):
+        keep = np.ones(64, bool)
+        if ph in used:
+            b, j, a, z = used[ph]
+            keep[a:z] = False
+            keys = kk[ph][:, :z]
+            lo, hi = O.kv.bf16(keys.min(1), "down"), O.kv.bf16(keys.max(1), "up")
+            assert np.array_equal(bd[ph][:, 0], lo) and np.array_equal(bd[ph][:, 1], hi), (ph, a, z)
+        else:
+            assert np.array_equal(bd[ph], bd0[ph], equal_nan=True)
+        assert np.array_equal(kk[ph][:, keep], k0[ph][:, keep], equal_nan=True)
+        assert np.array_equal(vv[ph][:, keep], v0[ph][:, keep], equal_nan=True)
+
+
+def test_append_far_positions_and_default_rows():
+    """Angles of positions far beyond 2^24 in fp32 steps; no cu_new: one row a sequence."""
+    g = _g()
+    H = Hkv = 1
+    hd, W = 128, 1 << 16
+    lens = [W * 64, W * 64 - 777]      # 4.2 million tokens
+    table = np.zeros((2, W))
+    table[0, (lens[0] - 1) // 64], table[1, (lens[1] - 1) // 64] = 1, 2
+    cache = g.KVCache(3, Hkv, hd, bits=8, device=DEV)
+    raw = torch.from_numpy(synth.normal((2, 3 * hd), 5)).bfloat16()
+    q = cache.append(g.KVBatch(i32(table), i32(lens)), raw.to(DEV), H, qk_norm=False)
+    g.model.sync_status(DEV)
+    inv = 10000.0 ** (-2.0 * np.arange(hd // 2) / hd)
+    for b in range(2):
+        x = raw[b].double().numpy()[:hd]
+        ref = O.rope(x[None], (lens[b] - 1) * inv[None])[0]
+        assert np.all(np.abs(f64(q)[b] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -20 * np.abs(x).max())
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_append_non_finite_zero_and_tiny_rows(bits):
+    g = _g()
+    hd, n = 128, 8
+    raw = synth.normal((n, 3 * hd), 6)
+    raw[1, hd + 3], raw[2, 2 * hd + 100], raw[3, hd:] = np.inf, np.nan, 0.0
+    raw[4, hd:] = 1e-38
+    raw[5, hd:] *= 1e30
+    cache = g.KVCache(1, 1, hd, bits=bits, device=DEV)
+    batch = g.KVBatch(i32([[0]]), i32([n]), i32([0, n]), max_new=n)
+    rawb = torch.from_numpy(raw.astype(np.float32)).bfloat16()
+    cache.append(batch, rawb.to(DEV), 1, rope=False, qk_norm=False)
+    k, v = (f64(t)[:, 0] for t in cache.read(batch, n))
+    g.model.sync_status(DEV)
+    x = rawb.double().numpy()
+    for got, ref in ((k, x[:, hd:2 * hd]), (v, x[:, 2 * hd:])):
+        _, _, val = O.kv.quantise(ref, bits)
+        assert np.array_equal(np.isnan(got), np.isnan(val))
+        f = np.isfinite(val)
+        assert np.all(np.abs(got - val)[f] <= 2.0 ** -8 * np.abs(val)[f])
+    b = f64(cache.bounds)[0, 0]
+    assert np.all(np.isnan(b[:, :64]))           # the infinite key's group
+    assert np.all(np.isnan(b[:, 64:])) == (bits == 8)
+
+
+def test_read_part_of_a_sequence():
+    w = World(4, 128, 2, [200, 90], 3)
+    b, cu = w.batch([37, 90])
+    k, v = w.cache.read(b, 127)
+    _g().model.sync_status(DEV)
+    for got, ref in ((f64(k), w.k), (f64(v), w.v)):
+        want = np.concatenate((ref[0][163:], ref[1]))
+        assert np.all(np.abs(got - want) <= 2.0 ** -8 * np.abs(want))
+
+
+# ---------------------------------------------------------------------------- attention
+
+ATTEND = [
+    # bits, hd, H, Hkv, lens, new, window
+    (8, 128, 2, 2, [1, 31, 32, 33, 64, 65, 700], [1] * 7, -1),
+    (4, 128, 2, 2, [1, 31, 32, 33, 64, 65, 700], [1] * 7, -1),
+    (4, 64, 3, 3, [1, 31, 32, 33, 64, 65, 700], [1] * 7, -1),
+    (8, 64, 3, 3, [1, 31, 32, 33, 64, 65, 700], [1] * 7, -1),
+    (8, 128, 4, 2, [5, 300, 64, 0, 129], [5, 3, 0, 0, 1], -1),      # no new tokens, no tokens
+    (4, 128, 8, 1, [70, 1], [2, 1], -1),                            # 16 rows: two column tiles
+    (8, 128, 20, 1, [130, 33], [1, 1], -1),                         # 20 query heads a kv head
+    (4, 64, 9, 1, [200], [7], -1),                                  # 63 rows: several tiles
+    (8, 64, 2, 2, [260], [260], -1),                                # a whole prompt
+    (4, 128, 2, 2, [500, 40], [3, 2], 0),
+    (8, 128, 2, 2, [500, 40], [3, 2], 31),
+    (4, 64, 4, 2, [500, 40], [9, 2], 100),
+    (8, 64, 4, 2, [500, 600], [40, 1], 64),
+    (4, 128, 1, 1, [5000], [1], -1),                                # one head cut between many workers
+    (8, 128, 13, 13, [900] * 3, [1] * 3, -1),
+]
+
+
+@pytest.mark.parametrize("case", ATTEND)
+def test_attention_matches_the_oracle(case):
+    bits, hd, H, Hkv, lens, new, window = case
+    w = World(bits, hd, Hkv, lens, 40)
+    batch, cu = w.batch(new)
+    M = sum(new)
+    q = bf(normal((M + 2, H * hd), 4))
+    o = torch.full((M + 2, H * hd), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((M + 2, H), 7.0, device=DEV)
+    w.cache.attend(batch, q, window=window, o=o, lse=lse)
+    _g().model.sync_status(DEV)
+    assert torch.all(o[M:] == 7.0) and torch.all(lse[M:] == 7.0)
+    check_attend(w, new, f64(q), f64(o), f64(lse), window=window)
+    again = w.cache.attend(batch, q, window=window)
+    assert torch.equal(again[0][:M], o[:M]) and torch.equal(again[1][:M], lse[:M])
+
+
+@pytest.mark.parametrize("qs,kvs", [(1e-20, 1.0), (1e12, 1e-12), (30.0, 1.0), (1.0, 1e20), (1.0, 1e-25), (0.0, 1.0)])
+def test_attention_over_a_wide_range_of_magnitudes(qs, kvs):
+    for bits in (4, 8):
+        w = World(bits, 128, 1, [150], 50, scale=kvs)
+        batch, _ = w.batch([2])
+        q = bf(normal((2, 128), 4) * qs / (kvs if kvs > 1 else 1.0))
+        o, lse = w.cache.attend(batch, q)
+        _g().model.sync_status(DEV)
+        check_attend(w, [2], f64(q), f64(o), f64(lse), what=(bits, qs, kvs))
+
+
+def test_attention_with_growing_scores_and_scales():
+    """Keys whose scores climb by hundreds and values whose scale climbs by powers of two: the running
+    maximum and the values' unit move again and again, between warps' parts too."""
+    for bits in (4, 8):
+        w = World(bits, 128, 1, [640], 51)
+        ramp = np.linspace(-3, 3, 640)[:, None, None]
+        qv = normal((128,), 9)
+        xk = w.k[0] * 0.05 + ramp * qv
+        xv = w.v[0] * 2.0 ** np.floor(np.linspace(-20, 20, 640))[:, None, None]
+        kc, ks, w.k[0] = O.kv.quantise(xk, bits)
+        vc, vs, w.v[0] = O.kv.quantise(xv, bits)
+        for j in range(10):
+            sl = slice(64 * j, 64 * j + 64)
+            tile = O.kv.pack(*(a[sl].transpose(1, 0, 2) for a in (kc, ks, vc, vs)), bits)
+            w.cache.tiles[w.table[0, j]] = torch.from_numpy(tile).to(DEV)
+        batch, _ = w.batch([1])
+        q = bf(qv[None])
+        o, lse = w.cache.attend(batch, q)
+        _g().model.sync_status(DEV)
+        check_attend(w, [1], f64(q), f64(o), f64(lse), what=bits)
+        o, lse = w.cache.attend(batch, -q)
+        check_attend(w, [1], -f64(q), f64(o), f64(lse), what=bits)
+
+
+def test_non_finite_queries_keys_and_values_show_in_their_rows_only():
+    w = World(8, 128, 2, [100, 100], 60)
+    g = _g()
+    R, ng, recb = O.kv.geometry(8, 128)
+    batch, _ = w.batch([2, 2])
+    q0 = normal((4, 256), 4)
+    q = bf(q0)
+    base = w.cache.attend(batch, q)[0].clone()
+    q2 = q.clone()
+    q2[1, 5], q2[2, 200] = float("nan"), float("inf")
+    o, lse = w.cache.attend(batch, q2)
+    bad = torch.zeros((4, 2), dtype=torch.bool, device=DEV)
+    bad[1, 0] = bad[2, 1] = True
+    assert torch.equal(torch.isnan(o.view(4, 2, 128)).all(-1), bad) and torch.equal(torch.isnan(lse), bad)
+    assert torch.equal(o.view(4, 2, 128)[~bad], base.view(4, 2, 128)[~bad])
+    # key 99 of sequence 0, head 1 is NaN: only the token at 99 sees it
+    tile = w.cache.tiles[w.table[0, 1], 1]
+    at = recb + 2 * 32 * R + 2 * (99 - 96)
+    tile[at:at + 2] = 255
+    o, _ = w.cache.attend(batch, q)
+    bad[:] = False
+    bad[1, 1] = True
+    assert torch.equal(torch.isnan(o.view(4, 2, 128)).any(-1), bad)
+    assert torch.equal(o.view(4, 2, 128)[~bad], base.view(4, 2, 128)[~bad])
+    g.model.sync_status(DEV)
+
+
+def test_bad_block_numbers_give_nan_rows_and_a_status():
+    w = World(4, 64, 2, [200, 130, 64], 61)
+    g = _g()
+    good, _ = w.batch([1, 1, 1])
+    q = bf(normal((3, 256), 4))
+    o0, l0 = w.cache.attend(good, q)
+    g.model.sync_status(DEV)
+    for value in (w.n_blocks, -1, 2 ** 31 - 1, -2 ** 31):
+        table = w.table.copy()
+        table[1, 1] = value
+        table[2, 1] = value      # not visible: never looked at
+        batch = g.KVBatch(i32(table), i32(w.lens), i32([0, 1, 2, 3]))
+        o, lse = w.cache.attend(batch, q)
+        with pytest.raises(g.GptError) as e:
+            g.model.sync_status(DEV)
+        assert e.value.code == 1
+        assert torch.isnan(o[1]).all() and torch.isnan(lse[1]).all()
+        assert torch.equal(o[[0, 2]], o0[[0, 2]]) or torch.allclose(o[[0, 2]].float(), o0[[0, 2]].float(), rtol=2e-2)
+        k, v = w.cache.read(g.KVBatch(i32(table), i32(w.lens), i32([0, 0, 130, 130]), max_new=130), 130)
+        with pytest.raises(g.GptError):
+            g.model.sync_status(DEV)
+        nan = np.zeros(130, bool)
+        nan[64:128] = True
+        assert np.array_equal(np.isnan(f64(k)).all((1, 2)), nan) and np.array_equal(np.isnan(f64(v)).any((1, 2)), nan)
+        before = w.cache.tiles.clone()
+        raw = torch.zeros((1, 4 * 64 + 2 * 128), dtype=torch.bfloat16, device=DEV)
+        t2 = i32([[value, value]])
+        w.cache.append(g.KVBatch(t2, i32([65])), raw, 4)
+        with pytest.raises(g.GptError):
+            g.model.sync_status(DEV)
+        assert torch.equal(w.cache.tiles, before)
+
+
+@pytest.mark.parametrize("lens,cu,max_new", [
+    ([200, 10 ** 6, 64], [0, 1, 2, 3], 1),        # longer than its block table
+    ([200, -5, 64], [0, 1, 2, 3], 1),
+    ([200, 130, 64], [0, 1, 9, 10], 1),           # more new tokens than max_new
+    ([200, 2, 64], [0, 1, 5, 6], 4),              # more new tokens than tokens
+    ([200, 130, 64], [0, 1, 0, 1], 1),            # rows that run backwards
+    ([200, 130, 64], [0, 1, 2 ** 31 - 1, -2 ** 31], 1),
+])
+def test_sequences_out_of_range_are_left_out(lens, cu, max_new):
+    """Sequence 1 of three is broken: it is reported, none of its rows is written, sequence 0 is right
+    (unless another sequence claims its row as well: cu = 0, 1, 0, 1 gives row 0 to sequences 0 and 2,
+    and it holds either's result)."""
+    w = World(8, 64, 1, [200, 130, 64], 62)
+    g = _g()
+    q = bf(normal((12, 128), 4))
+    batch = g.KVBatch(i32(w.table), i32(lens), i32(cu), max_new=max_new)
+    o = torch.full_like(q, 7.0)
+    lse = torch.full((12, 2), 7.0, device=DEV)
+    w.cache.attend(batch, q, o=o, lse=lse)
+    with pytest.raises(g.GptError) as e:
+        g.model.sync_status(DEV)
+    assert e.value.code == 1
+    if cu[2:] != [0, 1]:
+        check_attend(w, [1, 0, 0], f64(q), f64(o), f64(lse))
+    assert torch.all(o[1] == 7.0)
+    k, v = w.cache.read(batch, 12)
+    with pytest.raises(g.GptError):
+        g.model.sync_status(DEV)
+    if cu[2:] != [0, 1]:
+        assert np.all(np.abs(f64(k)[0] - w.k[0][199]) <= 2.0 ** -8 * np.abs(w.k[0][199]))
+    before = w.cache.tiles.clone()
+    w.cache.append(g.KVBatch(i32(w.table[1:2]), i32(lens[1:2]), i32(cu[1:3]), max_new=max_new),
+                   torch.zeros((12, 4 * 64), dtype=torch.bfloat16, device=DEV), 2)
+    with pytest.raises(g.GptError):
+        g.model.sync_status(DEV)
+    assert torch.equal(w.cache.tiles, before)
+    blocks, _ = w.cache.select(batch, q, 3)
+    with pytest.raises(g.GptError):
+        g.model.sync_status(DEV)
+    w.cache.attend(batch, q, blocks=torch.zeros((12, 1, 2), dtype=torch.int32, device=DEV))
+    with pytest.raises(g.GptError):
+        g.model.sync_status(DEV)
+    if cu[2:] != [0, 1]:
+        chosen = blocks[0, 0].tolist()
+        assert chosen[0] == 0 and chosen[2] == 3 and chosen[1] in (1, 2)
+
+
+def test_many_entries_use_the_scan_launch():
+    """More than 512 sequences, and more than 512 tiles of a prompt."""
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(0, 90, 700)]
+    new = [min(1, n) for n in lens]
+    w = World(4, 64, 1, lens, 63)
+    batch, _ = w.batch(new, max_new=1)
+    q = bf(normal((sum(new), 64), 4))
+    o, lse = w.cache.attend(batch, q)
+    _g().model.sync_status(DEV)
+    check_attend(w, new, f64(q), f64(o), f64(lse))
+    w = World(8, 64, 1, [1100], 64)
+    batch, _ = w.batch([1040])
+    q = bf(normal((1040, 512), 4))
+    o, lse = w.cache.attend(batch, q, window=50)
+    _g().model.sync_status(DEV)
+    check_attend(w, [1040], f64(q), f64(o), f64(lse), window=50)
+
+
+def test_blocks_beyond_four_gigabytes():
+    """Tiles whose byte offsets pass 2^32."""
+    g = _g()
+    bits, hd, Hkv = 8, 128, 10
+    small = World(bits, hd, Hkv, [300], 65)
+    far = (1 << 32) // (Hkv * 2 * O.kv.geometry(bits, hd)[2]) + 11
+    cache = g.KVCache(far + small.n_blocks, Hkv, hd, bits=bits,
+                      tiles=torch.empty((far + small.n_blocks, Hkv, small.cache.tiles.shape[2]), dtype=torch.uint8,
+                                        device=DEV), bounds=True)
+    cache.tiles[far:] = small.cache.tiles
+    cache.bounds[far:] = small.cache.bounds
+    table = np.where(small.table >= 0, small.table + far, -1)
+    batch = g.KVBatch(i32(table), i32([300]), i32([0, 2]), max_new=2)
+    q = bf(normal((2, Hkv * hd), 4))
+    o, lse = cache.attend(batch, q)
+    b2, _ = small.batch([2])
+    o2, lse2 = small.cache.attend(b2, q)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    raw = bf(normal((2, 3 * Hkv * hd), 5))
+    cache.append(batch, raw, Hkv)
+    small.cache.append(b2, raw, Hkv)
+    k, v = cache.read(batch, 2)
+    k2, v2 = small.cache.read(b2, 2)
+    assert torch.equal(k, k2) and torch.equal(v, v2)
+    assert torch.equal(cache.bounds[far:].view(torch.int16), small.cache.bounds.view(torch.int16))
+    assert torch.equal(cache.select(batch, q, 3)[0], small.cache.select(b2, q, 3)[0])
+    g.model.sync_status(DEV)
+
+
+# ---------------------------------------------------------------------------- selection
+
+SELECT = [
+    # bits, hd, H, Hkv, lens, new, n_select, n_first, n_last
+    (4, 128, 2, 2, [1, 64, 65, 1000, 0], [1, 1, 1, 1, 0], 4, 1, 1),
+    (8, 64, 4, 2, [700, 130], [3, 5], 5, 0, 0),
+    (8, 128, 8, 1, [900, 64], [2, 1], 1, 0, 1),
+    (4, 64, 3, 3, [1500], [1], 9, 2, 3),
+    (8, 64, 32, 1, [300], [1], 3, 0, 0),
+    (8, 64, 1, 1, [200], [1], 50, 1, 1),           # more than there are
+]
+
+
+@pytest.mark.parametrize("case", SELECT)
+def test_selection_matches_the_oracle_and_feeds_attention(case):
+    bits, hd, H, Hkv, lens, new, n, n_first, n_last = case
+    w = World(bits, hd, Hkv, lens, 70)
+    batch, cu = w.batch(new)
+    M = sum(new)
+    q = bf(normal((M + 1, H * hd), 4))
+    blocks = torch.full((M + 1, Hkv, n), 77, dtype=torch.int32, device=DEV)
+    scores = torch.full((M + 1, Hkv, w.W), 77.0, device=DEV)
+    w.cache.select(batch, q, n, n_first=n_first, n_last=n_last, blocks=blocks, scores=scores)
+    o, lse = w.cache.attend(batch, q, blocks=blocks)
+    _g().model.sync_status(DEV)
+    assert torch.all(blocks[M] == 77) and torch.all(scores[M] == 77.0)
+    got, sc, qf = blocks.cpu().numpy(), f64(scores), f64(q)
+    for b, m0 in enumerate(cu[:-1]):
+        for i in range(new[b]):
+            nb = (lens[b] - new[b] + i) // 64 + 1
+            ref = O.kv.block_scores(qf[m0 + i].reshape(H, hd), w.bounds[w.table[b, :nb]])
+            assert np.all(np.abs(sc[m0 + i, :, :nb] - ref) <= 2.0 ** -24 * np.abs(ref) + 1e-300)
+            assert np.all(sc[m0 + i, :, nb:] == -np.inf)
+            for h in range(Hkv):
+                want = O.kv.choose(sc[m0 + i, h, :nb], n, n_first, n_last)
+                assert got[m0 + i, h].tolist() == want + [-1] * (n - len(want))
+    check_attend(w, new, qf, f64(o), f64(lse), sel=got)
+
+
+def test_selection_ties_and_nan_scores():
+    w = World(8, 64, 1, [64 * 600], 71)
+    g = _g()
+    batch, _ = w.batch([1])
+    w.cache.bounds.zero_()
+    q = bf(np.ones((1, 64)))
+    top = [3, 77, 300, 301, 555]
+    for j in top:
+        w.cache.bounds[w.table[0, j]] = 1.0
+    blocks, scores = w.cache.select(batch, q, 8, n_first=0, n_last=0)
+    assert blocks[0, 0].tolist() == [0, 1, 2, 3, 77, 300, 301, 555]
+    blocks, _ = w.cache.select(batch, q, 3, n_first=0, n_last=1)
+    assert blocks[0, 0].tolist() == [3, 77, 599]
+    w.cache.bounds[w.table[0, 400]] = float("nan")
+    w.cache.bounds[w.table[0, 7]] = -1.0
+    blocks, scores = w.cache.select(batch, q, 2, n_first=0, n_last=1)
+    assert blocks[0, 0].tolist() == [400, 599] and torch.isnan(scores[0, 0, 400])
+    blocks, _ = w.cache.select(batch, -q, 300, n_first=0, n_last=0)    # -1, 0 and 1 change places
+    got = blocks[0, 0].tolist()
+    assert 7 in got and 400 in got and not set(top) & set(got) and got == sorted(got)
+    rest = [j for j in range(600) if j not in top and j not in (7, 400)][:298]
+    assert got == sorted(rest + [7, 400])
+    g.model.sync_status(DEV)
+
+
+def test_attention_over_a_list_of_the_callers_own():
+    """Entries that are negative or not visible are passed over; one listed twice counts twice."""
+    w = World(4, 128, 2, [400, 130], 72)
+    g = _g()
+    batch, _ = w.batch([2, 1])
+    q = bf(normal((3, 512), 4))
+    sel = np.full((3, 2, 6), -1)
+    sel[0, 0] = [2, -1, 2, 99, 0, 5]
+    sel[0, 1] = [-5, -1, -1, -1, -1, -1]           # nothing: a row without keys
+    sel[1, 0] = [6, 5, 4, 3, 2, 1]
+    sel[1, 1] = [6, 7, -1, 6, 6, 0]
+    sel[2, 0] = [2, 1, 0, 2, 2, 2]                 # three are visible: three entries are read
+    sel[2, 1] = [1, 3, 2, 0, 0, 0]
+    o, lse = w.cache.attend(batch, q, blocks=i32(sel))
+    g.model.sync_status(DEV)
+    check_attend(w, [2, 1], f64(q), f64(o), f64(lse), sel=sel)
+
+
+# ---------------------------------------------------------------------------- together
+
+@pytest.mark.parametrize("bits,hd,H,Hkv", [(8, 128, 2, 2), (4, 64, 4, 2)])
+def test_a_layer_answers_step_by_step(bits, hd, H, Hkv):
+    """A prompt, then single tokens: each step appends, selects and attends, and must equal the
+    oracle's attention over the values the cache holds; and with everything in view, the prompt's rows
+    come near the framework's own attention over unquantised keys (8 bits: the quantiser's half step,
+    1/254 of a row's largest, against scores of order one)."""
+    g = _g()
+    n0, steps = 150, 70
+    total = n0 + steps
+    raw = torch.from_numpy(synth.normal((total, (H + 2 * Hkv) * hd), 8)).bfloat16().to(DEV)
+    cache = g.KVCache(8, Hkv, hd, bits=bits, device=DEV)
+    table = i32([[5, 2, 7, 0]])
+    lens, cu = i32([n0]), i32([0, n0])
+    prompt = g.KVBatch(table, lens, cu, max_new=n0)
+    q = cache.append(prompt, raw[:n0].contiguous(), H)
+    o, lse = cache.attend(prompt, q)
+    w = World.__new__(World)
+    w.bits, w.hd, w.Hkv, w.W = bits, hd, Hkv, 4
+
+    def held():
+        k, v = O.kv.unpack(cache.tiles.cpu().numpy()[[5, 2, 7, 0]], bits, hd)
+        w.lens = [int(lens.item())]
+        w.k = [k.transpose(0, 2, 1, 3).reshape(-1, Hkv, hd)[:w.lens[0]]]
+        w.v = [v.transpose(0, 2, 1, 3).reshape(-1, Hkv, hd)[:w.lens[0]]]
+
+    held()
+    check_attend(w, [n0], f64(q), f64(o), f64(lse))
+    if bits == 8 and H == Hkv:
+        f = g.ops.attention_fwd(raw[:n0].contiguous(), 1, n0, H, hd)
+        d = (f["o"].float() - o.float())
+        assert d.norm() <= 2e-2 * f["o"].float().norm()
+    one = g.KVBatch(table, lens)
+    for t in range(n0, total):
+        lens.fill_(t + 1)
+        q = cache.append(one, raw[t:t + 1].contiguous(), H)
+        o, lse = cache.attend(one, q)
+        blocks, _ = cache.select(one, q, 2, n_first=0, n_last=1)
+        so, sl = cache.attend(one, q, blocks=blocks)
+        if t % 23 == 0 or t == total - 1:
+            held()
+            check_attend(w, [1], f64(q), f64(o), f64(lse), what=t)
+            check_attend(w, [1], f64(q), f64(so), f64(sl), sel=blocks.cpu().numpy(), what=t)
+    g.model.sync_status(DEV)
+
+
+def test_a_captured_step_replays_with_new_contents():
+    g = _g()
+    H = Hkv = 2
+    hd = 128
+    w = World(8, hd, Hkv, [190, 64, 300], 80)
+    lens, table = i32(w.lens), i32(w.table)
+    batch = g.KVBatch(table, lens)
+    raw = bf(normal((3, 3 * H * hd), 5))
+
+    def step():
+        q = w.cache.append(batch, raw, H)
+        blocks, scores = w.cache.select(batch, q, 3)
+        return (q, blocks, scores, *w.cache.attend(batch, q), *w.cache.attend(batch, q, blocks=blocks))
+
+    side = torch.cuda.Stream(DEV)
+    side.wait_stream(torch.cuda.current_stream(DEV))
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream(DEV).wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    tiles = w.cache.tiles.clone()
+    for seed, new_lens in ((6, [190, 64, 300]), (7, [100, 3, 257]), (8, [64, 1, 299])):
+        raw.copy_(bf(normal((3, 3 * H * hd), seed)))
+        lens.copy_(i32(new_lens))
+        w.cache.tiles.copy_(tiles)
+        w.cache.bounds.copy_(bf(w.bounds))
+        graph.replay()
+        got = [t.clone() for t in out]
+        w.cache.tiles.copy_(tiles)
+        w.cache.bounds.copy_(bf(w.bounds))
+        ref = step()
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
+    g.model.sync_status(DEV)
+
+
+def test_calls_on_two_streams_at_once():
+    g = _g()
+    w = World(4, 128, 4, [3000, 2500, 1800], 81)
+    batch, _ = w.batch([1, 1, 1])
+    qs = [bf(normal((3, 4 * 128), s)) for s in (4, 5)]
+    want = [[t.clone() for t in w.cache.attend(batch, q)] for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(DEV) for _ in qs]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(w.cache.attend(batch, qs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_binding_refuses_wrong_tensors():
+    g = _g()
+    w = World(8, 64, 2, [100], 82)
+    batch, _ = w.batch([1])
+    q = bf(normal((1, 256), 4))
+    for bad in (q.float(), q[:, :100].contiguous(), q.cpu(), bf(normal((1, 512), 4))[:, ::2]):
+        with pytest.raises(AssertionError):
+            w.cache.attend(batch, bad)
+    with pytest.raises(AssertionError):
+        w.cache.attend(batch, q, blocks=i32(np.zeros((1, 1, 3))))
+    with pytest.raises(AssertionError):
+        w.cache.append(batch, q, 4)
+    with pytest.raises(AssertionError):
+        g.KVBatch(batch.block_table, batch.lens.long())
+    with pytest.raises(AssertionError):
+        g.KVBatch(batch.block_table, batch.lens, max_new=3)
+    with pytest.raises(g.GptError):
+        w.cache.select(batch, q, 1, n_first=1, n_last=1)
+    with pytest.raises(g.GptError):
+        g.KVCache(4, 2, 64, bits=8, device=DEV, bounds=False).select(batch, q, 2)
+    with pytest.raises(g.GptError):
+        w.cache.attend(batch, q, scratch=torch.empty(256, dtype=torch.uint8, device=DEV))
