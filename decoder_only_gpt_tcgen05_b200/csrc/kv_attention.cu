@@ -16,8 +16,8 @@
 //     that arrived), and the legacy tensor path has the rate to spare.  Cache rows are the M side
 //     (S^T = K Q^T, O^T = V^T P^T), so a code fills one operand element and only the 8 query columns
 //     are padded.
-//   - A warp is a worker of its own: it takes an equal share of all (sequence, tile, head, 32-token
-//     record) units, fetches its records with bulk copies into a private ring, keeps running maximum,
+//   - A warp is a worker of its own: it takes an equal share of all (sequence, tile, head, step of 32
+//     or 64 tokens) units, fetches them with bulk copies into a private ring, keeps running maximum,
 //     sum and output in registers, and never waits for another warp.  Every worker has the same
 //     amount of work whatever the lengths; a (sequence, tile, head) that is cut between workers is
 //     joined, in order, by kv_join_kernel, so results do not depend on timing.
@@ -55,12 +55,18 @@ struct AttendArgs {
 struct KvEntry {
   int b, row0, rho0, nrows;  // query row rho of the tile: token row0 + rho / G, head h G + rho mod G
   int pos0;                  // position of token row0
-  int jlo, nrec;             // first record and how many (sparse: two for each listed block)
+  int jlo, nrec;             // first unit of U keys, and how many (sparse: 64 / U for each listed block)
   int nb;                    // visible blocks (sparse)
 };
 
+// Where a worker is: the entry, the head, the first of its units that it took, and the positions of the
+// tile's first and last query row.
+struct KvSpan {
+  int e, h, j_first, p_lo, p_hi;
+};
+
 template <bool SPARSE>
-__device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, bool report) {
+__device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, int U, bool report) {
   KvEntry t;
   const int unit = e / p.QT;
   t.rho0 = (e - unit * p.QT) * RT;
@@ -91,10 +97,10 @@ __device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, 
   const int lo = t.pos0 + t.rho0 / p.G, hi = t.pos0 + (t.rho0 + t.nrows - 1) / p.G;
   if (SPARSE) {
     t.nb = lo / kKvBlock + 1;
-    t.nrec = 2 * min(p.n_sel, t.nb);
+    t.nrec = kKvBlock / U * min(p.n_sel, t.nb);
   } else {
-    t.jlo = p.window < 0 ? 0 : max(0, lo - p.window) / kKvRec;
-    t.nrec = hi / kKvRec - t.jlo + 1;
+    t.jlo = p.window < 0 ? 0 : max(0, lo - p.window) / U;
+    t.nrec = hi / U - t.jlo + 1;
   }
   return t;
 }
@@ -104,13 +110,21 @@ __device__ __forceinline__ long long worker_of(long long f, long long total, lon
   return ((f + 1) * workers - 1) / total;
 }
 
+// d = A B + (c0, c1, c0, c1): the accumulator's start is the same in both row halves
 __device__ __forceinline__ void mma_f16(float (&d)[4], unsigned int a0, unsigned int a1, unsigned int a2,
-                                        unsigned int a3, unsigned int b0, unsigned int b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
+                                        unsigned int a3, const unsigned int (&b)[2], float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
+      "%10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1));
+}
+// d += A B
+__device__ __forceinline__ void mma_f16(float (&d)[4], unsigned int a0, unsigned int a1, unsigned int a2,
+                                        unsigned int a3, const unsigned int (&b)[2]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, "
       "%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]));
 }
 // transpose of an 8 x 8 matrix of halves held as one mma fragment register
 __device__ __forceinline__ unsigned int transpose8(unsigned int x) {
@@ -125,43 +139,64 @@ __device__ __forceinline__ unsigned int pack_h2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_h2(unsigned int u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
-// 16 bytes of shared memory; HOLD keeps the read where it is written (a kernel short of registers)
-template <bool HOLD>
-__device__ __forceinline__ uint4 lds16(const uint8_t* p) {
-  if (!HOLD) return *reinterpret_cast<const uint4*>(p);
-  uint4 v;
+// Shared-memory reads by 32-bit address, kept where they are written: hoisted by the compiler they
+// would all be live at once, and the kernel is short of registers.
+__device__ __forceinline__ void lds16(uint32_t a, unsigned int* v) {
   asm volatile("ld.volatile.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(smem_u32(p))
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(a)
                : "memory");
+}
+__device__ __forceinline__ void lds8(uint32_t a, unsigned int* v) {
+  asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ unsigned int lds4(uint32_t a) {
+  unsigned int v;
+  asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ unsigned int lds2(uint32_t a) {
+  unsigned short v;
+  asm volatile("ld.volatile.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
   return v;
 }
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((unsigned int)(e + 127) << 23); }  // -126..127
 
-constexpr int kAttendWarps = 4;
 constexpr int kAttendMaxWorkers = 160 * 16;
 constexpr int kScanSmem = 512;  // entries scanned by every CTA itself
 
-// Ring depth and CTAs an SM: about 200 KB of shared memory in flight, far above the 44 KB an SM needs
-// in flight to cover HBM's latency, split so that the register budget allows as many warps as fit.
+// Keys of a unit (U), ring depth and CTAs an SM.  A unit is one fetch: 64 keys, or 32 for 128-wide
+// 8-bit rows, whose 64 would leave room for too few warps.  The rings hold about 200 KB an SM, far above
+// the 44 KB that cover HBM's latency; 12 warps an SM leave each thread the 168 registers that one query
+// column tile needs, 8 warps the 255 of two.
 template <class G, int NT>
 struct AttendCfg {
-  static constexpr int STAGES = G::REC > 8000 ? 2 : G::REC > 2200 ? 3 : 4;
-  static constexpr int CTAS = NT > 1 ? 2 : 3;
-  static constexpr int RING = STAGES * G::REC;
-  static constexpr int SMEM = kAttendWarps * RING;
+  static constexpr int U = G::REC > 8000 ? 32 : 64;
+  static constexpr int WARPS = 4;
+  static constexpr int CTAS = (NT > 1 ? 2 : 3) + (G::HD == 64);
+  static constexpr int STAGE = U / kKvRec * G::REC;
+  static constexpr int FIT = 220 * 1024 / (WARPS * CTAS * STAGE);
+  static constexpr int STAGES = FIT < 4 ? 2 : 4;  // a power of two
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int SMEM = WARPS * RING;
 };
 
 template <class G, int NT, bool SPARSE>
-__global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_attend_kernel(AttendArgs p) {
+__global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>::CTAS) kv_attend_kernel(AttendArgs p) {
   using C = AttendCfg<G, NT>;
   constexpr int HD = G::HD, NG = G::NG, RT = 8 * NT, MT = HD / 16, KW = G::KB / 4, VW = G::VB / 4;
+  constexpr int U = C::U, TL = 2 / NT;  // keys of a unit; 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
-  __shared__ uint64_t bars[kAttendWarps][C::STAGES];
-  __shared__ int meta[kAttendWarps][C::STAGES];
+  __shared__ uint64_t bars[C::WARPS][C::STAGES];
+  __shared__ int meta[C::WARPS][C::STAGES];
   __shared__ long long s_pre[kScanSmem + 1];
-  __shared__ long long s_warp[kAttendWarps];
-  __shared__ KvEntry s_ent[kAttendWarps];
+  __shared__ long long s_warp[C::WARPS];
+  // Of the computing and the fetching iterator: what is the same for a whole (entry, head) lives in
+  // shared memory, written by lane 0, since the registers are needed for the step.
+  __shared__ KvEntry s_ent[C::WARPS], s_fent[C::WARPS];
+  __shared__ KvSpan s_span[C::WARPS];
+  __shared__ int s_pos[C::WARPS][RT];
+  __shared__ long long s_row[C::WARPS][RT];
   __shared__ int abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c = lane & 3;
   if (lane == 0) {
@@ -177,9 +212,9 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
   if (!p.scanned) {
     pre = s_pre;
     long long run = 0;
-    for (int e0 = 0; e0 < p.E; e0 += kAttendWarps * 32) {
+    for (int e0 = 0; e0 < p.E; e0 += C::WARPS * 32) {
       const int e = e0 + tid;
-      long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, blockIdx.x == 0).nrec : 0;
+      long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, U, blockIdx.x == 0).nrec : 0;
       const long long own = v;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -189,7 +224,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
       if (lane == 31) s_warp[warp] = v;
       __syncthreads();
       long long before = run;
-      for (int x = 0; x < kAttendWarps; ++x) {
+      for (int x = 0; x < C::WARPS; ++x) {
         if (x < warp) before += s_warp[x];
         run += s_warp[x];
       }
@@ -208,7 +243,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
 
   // ---- this warp's share
   const long long total = pre[p.E] * p.Hkv;
-  const long long workers = min((long long)gridDim.x * kAttendWarps, total);
+  const long long workers = min((long long)gridDim.x * C::WARPS, total);
   const int w = warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
   if (w >= workers) return;
   const long long ua = w * total / workers;
@@ -229,37 +264,36 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
     fh = (int)(r / n);
     fj = (int)(r - fh * n);
   }
-  int e = fe, h = fh, j = fj;  // the computing iterator
-  int f_b, f_row, f_jlo, f_nrec, f_nb;  // of its entry: sequence, token row (sparse), records, blocks
+  int j = fj;  // the computing iterator's unit; its entry and head are in sp
+  KvSpan& sp = s_span[warp];
   int f_phys = 0, f_kb = 0, f_next = -1;
-  auto f_enter = [&](const KvEntry& t) {
-    f_b = t.b, f_row = t.row0, f_jlo = t.jlo, f_nrec = t.nrec, f_nb = t.nb;
-  };
+  const KvEntry& ft = s_fent[warp];
   // loads the block number of unit (fe, fh, fj); `fresh`: the listed block was not loaded ahead
   auto look_up = [&](bool fresh) {
     int blk;
     if (SPARSE) {
-      if ((fj & 1) && !fresh) {
-        f_kb += f_kb >= 0 ? kKvRec : 0;
+      constexpr int PER = kKvBlock / U;  // units of a listed block
+      if (fj % PER && !fresh) {
+        f_kb += f_kb >= 0 ? U : 0;
         return;
       }
-      const int* list = p.sel + ((long long)f_row * p.Hkv + fh) * p.n_sel + (fj >> 1);
+      const int* list = p.sel + ((long long)ft.row0 * p.Hkv + fh) * p.n_sel + fj / PER;
       blk = fresh ? list[0] : f_next;
-      f_next = fj + 2 < f_nrec ? list[1] : -1;
-      if (blk < 0 || blk >= f_nb) {
+      f_next = fj + PER < ft.nrec ? list[1] : -1;
+      if (blk < 0 || blk >= ft.nb) {
         f_kb = -1;
         return;
       }
-      f_kb = blk * kKvBlock + (fj & 1) * kKvRec;
+      f_kb = blk * kKvBlock + fj % PER * U;
     } else {
-      f_kb = (f_jlo + fj) * kKvRec;
+      f_kb = (ft.jlo + fj) * U;
       blk = f_kb / kKvBlock;
     }
-    f_phys = p.rows.table[(long long)f_b * p.rows.W + blk];
+    f_phys = p.rows.table[(long long)ft.b * p.rows.W + blk];
   };
-  int fetched = 0;
-  auto fetch = [&](int stage) {  // the next unit into the stage, then on to the one after it
-    if (fetched == units) return;
+  auto fetch = [&](int f) {  // this worker's unit f into its stage, then on to the one after it
+    if (f >= units) return;
+    const int stage = f % C::STAGES;
     if (lane == 0) {
       uint64_t* bar = &bars[warp][stage];
       if (f_kb < 0) {
@@ -271,14 +305,14 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
         mbar_arrive(bar);
       } else {
         meta[warp][stage] = f_kb;
-        mbar_expect_tx(bar, G::REC);
-        bulk_load(ring + stage * G::REC,
-                  p.tiles + ((long long)f_phys * p.Hkv + fh) * G::TILE + (f_kb / kKvRec & 1) * G::REC, G::REC, bar);
+        mbar_expect_tx(bar, C::STAGE);
+        bulk_load(ring + stage * C::STAGE,
+                  p.tiles + ((long long)f_phys * p.Hkv + fh) * G::TILE + f_kb % kKvBlock / U * C::STAGE, C::STAGE, bar);
       }
     }
-    if (++fetched == units) return;
+    if (f + 1 >= units) return;
     bool fresh = false;
-    if (++fj == f_nrec) {
+    if (++fj == ft.nrec) {
       fj = 0;
       fresh = true;
       if (++fh == p.Hkv) {
@@ -286,16 +320,18 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
         do {
           ++fe;
         } while (pre[fe + 1] == pre[fe]);
-        f_enter(kv_entry<SPARSE>(p, fe, RT, false));
+        __syncwarp();
+        const KvEntry t = kv_entry<SPARSE>(p, fe, RT, U, false);
+        if (lane == 0) s_fent[warp] = t;
+        __syncwarp();
       }
     }
     look_up(fresh);
   };
   {
-    const KvEntry t = kv_entry<SPARSE>(p, fe, RT, false);
-    if (lane == 0) s_ent[warp] = t;
+    const KvEntry t = kv_entry<SPARSE>(p, fe, RT, U, false);
+    if (lane == 0) s_ent[warp] = s_fent[warp] = t, sp.e = fe, sp.h = fh;
     __syncwarp();
-    f_enter(t);
   }
   look_up(true);
   for (int i = 0; i < C::STAGES; ++i) fetch(i);
@@ -305,41 +341,39 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
   const int window = SPARSE ? -1 : p.window;
   unsigned int qb[NT][MT][2];
   float csum[NT][NG][2], qmul[NT][2];  // accumulator start (-Z sum q), and q's scale times log2(e) / sqrt(hd)
-  int pcol[NT][2];
   float acc[NT][MT][4], m[NT][2], l[NT][2], vref = 0.f;  // vref: power of two, the values' unit
-  int j_first, p_lo, p_hi;  // positions of the tile's first and last query row
   auto begin = [&]() {
     const KvEntry t = s_ent[warp];
-    j_first = j;
-    p_lo = t.pos0 + t.rho0 / p.G;
-    p_hi = t.pos0 + (t.rho0 + t.nrows - 1) / p.G;
+    if (lane == 0) {
+      sp.j_first = j;
+      sp.p_lo = t.pos0 + t.rho0 / p.G;
+      sp.p_hi = t.pos0 + (t.rho0 + t.nrows - 1) / p.G;
+    }
+    if (lane < RT) {  // the tile's query rows: position and row of q and o (-1: none)
+      const int tok = (t.rho0 + lane) / p.G, g = t.rho0 + lane - tok * p.G;
+      s_pos[warp][lane] = lane < t.nrows ? t.pos0 + tok : -1;
+      s_row[warp][lane] = lane < t.nrows ? (long long)(t.row0 + tok) * p.H + sp.h * p.G + g : -1;
+    }
+    __syncwarp();
+    constexpr int PER = 32 / G::BITS;  // dims of a code word
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int n = nt * 8 + gid, rho = t.rho0 + n;
-      const bool live = n < t.nrows;
-      float x[HD / 4];
-      unsigned int top = 0;
-      const __nv_bfloat16* src =
-          p.q + ((long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G) * HD;
+      const long long row = s_row[warp][nt * 8 + gid];
+      unsigned int xw[HD / 8];  // this lane's quarter of the row as bf16 pairs
 #pragma unroll
       for (int wi = 0; wi < KW; ++wi) {
-        unsigned int u[4] = {0, 0, 0, 0};
-        if (live) {
-          if (G::BITS == 4) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(src + 32 * wi + 8 * c));
-            u[0] = v.x, u[1] = v.y, u[2] = v.z, u[3] = v.w;
-          } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(src + 16 * wi + 4 * c));
-            u[0] = v.x, u[1] = v.y;
-          }
-        }
-        constexpr int PER = 32 / G::BITS;  // dims of a word
-#pragma unroll
-        for (int y = 0; y < PER; ++y) {
-          x[wi * PER + y] = y & 1 ? bf16_hi(u[y >> 1]) : bf16_lo(u[y >> 1]);
-          top = max(top, __float_as_uint(x[wi * PER + y]) & 0x7fffffffu);
+        const __nv_bfloat16* src = p.q + row * HD + 4 * PER * wi + PER * c;
+        if (G::BITS == 4) {
+          const uint4 v = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          xw[4 * wi] = v.x, xw[4 * wi + 1] = v.y, xw[4 * wi + 2] = v.z, xw[4 * wi + 3] = v.w;
+        } else {
+          const uint2 v = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+          xw[2 * wi] = v.x, xw[2 * wi + 1] = v.y;
         }
       }
+      unsigned int top = 0;  // largest |x| as bits
+#pragma unroll
+      for (int i = 0; i < HD / 8; ++i) top = max(top, max((xw[i] << 16) & 0x7fffffffu, xw[i] & 0x7fff0000u));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       // the row times 2^(14 - ex) has its largest in [2^14, 2^15)
@@ -347,41 +381,28 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
       const int s1 = (14 - ex) / 2;
       const float f1 = exp2i(s1), f2 = exp2i(14 - ex - s1);
       const bool odd = (top >> 23) >= 127 + 117;  // beyond fp32's products, an infinity or a NaN
+      auto y = [&](int i) { return (i & 1 ? bf16_hi(xw[i >> 1]) : bf16_lo(xw[i >> 1])) * f1 * f2; };
       float sum[NG];
 #pragma unroll
       for (int g = 0; g < NG; ++g) sum[g] = 0.f;
 #pragma unroll
-      for (int wi = 0; wi < KW; ++wi) {
-        const int g = NG == 1 ? 0 : wi / 2;
-        if (G::BITS == 4) {
-          float y[8];
-#pragma unroll
-          for (int z = 0; z < 8; ++z) y[z] = x[wi * 8 + z] * f1 * f2;
-#pragma unroll
-          for (int z = 0; z < 2; ++z) {  // nibbles (0, 4), (1, 5) and (2, 6), (3, 7)
-            qb[nt][2 * wi + z][0] = pack_h2(y[2 * z], y[2 * z + 4]);
-            qb[nt][2 * wi + z][1] = pack_h2(y[2 * z + 1] * 0.0625f, y[2 * z + 5] * 0.0625f);
-            const float2 a = unpack_h2(qb[nt][2 * wi + z][0]), b = unpack_h2(qb[nt][2 * wi + z][1]);
-            sum[g] += (a.x + a.y) + 16.f * (b.x + b.y);
-          }
-        } else {
-          float y[4];
-#pragma unroll
-          for (int z = 0; z < 4; ++z) y[z] = x[wi * 4 + z] * f1 * f2;
-          qb[nt][wi][0] = pack_h2(y[0], y[2]);
-          qb[nt][wi][1] = pack_h2(y[1], y[3]);
-          const float2 a = unpack_h2(qb[nt][wi][0]), b = unpack_h2(qb[nt][wi][1]);
-          sum[g] += (a.x + a.y) + (b.x + b.y);
+      for (int k = 0; k < MT; ++k) {
+        const int g = NG == 1 ? 0 : k / 4;
+        unsigned int(&b)[2] = qb[nt][k];
+        if (G::BITS == 4) {  // word k / 2: nibbles (0, 4), (1, 5) or (2, 6), (3, 7)
+          const int at = k / 2 * 8 + k % 2 * 2;
+          b[0] = pack_h2(y(at), y(at + 4));
+          b[1] = pack_h2(y(at + 1) * 0.0625f, y(at + 5) * 0.0625f);
+        } else {  // word k: bytes (0, 2), (1, 3)
+          b[0] = pack_h2(y(4 * k), y(4 * k + 2));
+          b[1] = pack_h2(y(4 * k + 1), y(4 * k + 3));
         }
+        const float2 u = unpack_h2(b[0]), v = unpack_h2(b[1]);
+        sum[g] += (u.x + u.y) + (G::BITS == 4 ? 16.f : 1.f) * (v.x + v.y);
       }
       const float mul = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * exp2i(ex + 10);
-      const int pos = live ? t.pos0 + rho / p.G : -1;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int from = (2 * c + i) * 4;
-        qmul[nt][i] = __shfl_sync(0xffffffffu, mul, from);
-        pcol[nt][i] = __shfl_sync(0xffffffffu, pos, from);
-      }
+      for (int i = 0; i < 2; ++i) qmul[nt][i] = __shfl_sync(0xffffffffu, mul, (2 * c + i) * 4);
 #pragma unroll
       for (int g = 0; g < NG; ++g) {
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 1);
@@ -391,20 +412,19 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
           csum[nt][g][i] = __shfl_sync(0xffffffffu, sum[g], (2 * c + i) * 4) * (-G::Z * 5.9604644775390625e-8f);
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) m[nt][i] = -INFINITY, l[nt][i] = 0.f;
+      for (int i = 0; i < 2; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
 #pragma unroll
-      for (int x2 = 0; x2 < MT; ++x2)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][x2][i] = 0.f;
+        for (int k = 0; k < 4; ++k) acc[nt][i][k] = 0.f;
     }
     vref = 0.f;
   };
 
   // ---- end of one (entry, head) in this worker: the output, or this worker's part of it
   auto finish = [&]() {
-    const KvEntry t = s_ent[warp];
-    const bool whole = j_first == 0 && j == t.nrec - 1;
-    const int slot = j_first == 0 ? 1 : 0;
+    const bool whole = sp.j_first == 0 && j == s_ent[warp].nrec - 1;
+    const long long part0 = ((long long)(warp * gridDim.x + blockIdx.x) * 2 + (sp.j_first == 0 ? 1 : 0)) * p.RV;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -412,177 +432,172 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
         float sum = l[nt][i];
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int n = nt * 8 + 2 * c + i, rho = t.rho0 + n;
-        if (n >= t.nrows) continue;
-        // acc is in units of 2^-24 vref / 64; the rows of bits 4..7 in 16 times that
-        const float f = sum == 0.f ? 0.f : 262144.f * vref / sum;
-        const float lse2 = sum == 0.f ? -INFINITY : m[nt][i] + log2f(sum);
-        const long long qrow = (long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G;
-        const long long prow = (long long)(w * 2 + slot) * p.RV + n;
+        const int n = nt * 8 + 2 * c + i;
+        const long long qrow = s_row[warp][n];
+        if (qrow >= 0) {
+          // acc is in units of 2^-24 vref / 64; the rows of bits 4..7 in 16 times that
+          const float f = sum == 0.f ? 0.f : 262144.f * vref / sum;
+          const float lse2 = sum == 0.f ? -INFINITY : m[nt][i] + log2f(sum);
 #pragma unroll
-        for (int wj = 0; wj < HD / 64; ++wj) {
-          float v[8];
-          if (G::BITS == 4) {
+          for (int wj = 0; wj < HD / 64; ++wj) {
+            float v[8];
+            if (G::BITS == 4) {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              v[4 * x] = acc[nt][4 * wj + 2 * x][i] * f;
-              v[4 * x + 2] = acc[nt][4 * wj + 2 * x][2 + i] * f;
-              v[4 * x + 1] = acc[nt][4 * wj + 2 * x + 1][i] * (f * 0.0625f);
-              v[4 * x + 3] = acc[nt][4 * wj + 2 * x + 1][2 + i] * (f * 0.0625f);
+              for (int x = 0; x < 2; ++x) {
+                v[4 * x] = acc[nt][4 * wj + 2 * x][i] * f;
+                v[4 * x + 2] = acc[nt][4 * wj + 2 * x][2 + i] * f;
+                v[4 * x + 1] = acc[nt][4 * wj + 2 * x + 1][i] * (f * 0.0625f);
+                v[4 * x + 3] = acc[nt][4 * wj + 2 * x + 1][2 + i] * (f * 0.0625f);
+              }
+            } else {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                v[2 * x] = acc[nt][4 * wj + x][i] * f;
+                v[2 * x + 1] = acc[nt][4 * wj + x][2 + i] * f;
+              }
             }
-          } else {
+            if (whole) {
+              uint4 u;
+              unsigned int* uu = &u.x;
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              v[2 * x] = acc[nt][4 * wj + x][i] * f;
-              v[2 * x + 1] = acc[nt][4 * wj + x][2 + i] * f;
+              for (int x = 0; x < 4; ++x) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
+                uu[x] = *reinterpret_cast<const unsigned int*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(p.o + qrow * HD + 64 * wj + 8 * gid) = u;
+            } else {
+              float4* d = reinterpret_cast<float4*>(p.part_o + (part0 + n) * HD + 64 * wj + 8 * gid);
+              d[0] = make_float4(v[0], v[1], v[2], v[3]);
+              d[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
           }
-          if (whole) {
-            uint4 u;
-            unsigned int* uu = &u.x;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * x], v[2 * x + 1]);
-              uu[x] = *reinterpret_cast<const unsigned int*>(&b2);
-            }
-            *reinterpret_cast<uint4*>(p.o + qrow * HD + 64 * wj + 8 * gid) = u;
-          } else {
-            float4* d = reinterpret_cast<float4*>(p.part_o + prow * HD + 64 * wj + 8 * gid);
-            d[0] = make_float4(v[0], v[1], v[2], v[3]);
-            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (gid == 0) {
+            if (!whole) p.part_lse[part0 + n] = lse2;
+            else if (p.lse) p.lse[qrow] = lse2 * 0.6931471805599453f;
           }
         }
-        if (gid == 0) {
-          if (!whole) p.part_lse[prow] = lse2;
-          else if (p.lse) p.lse[qrow] = lse2 * 0.6931471805599453f;
-        }
+        __syncwarp();
       }
     }
   };
 
   begin();
-  int stage = 0, parity = 0;
   for (int u = 0; u < units; ++u) {
-    if (!mbar_wait(&bars[warp][stage], parity, p.ctl, &abort_flag, 20)) {
+    const int stage = u % C::STAGES;
+    if (!mbar_wait(&bars[warp][stage], u / C::STAGES & 1, p.ctl, &abort_flag, 20)) {
       // give up: the copies still in flight land in this CTA's shared memory, so wait for them too
-      for (int i = 1; i < C::STAGES; ++i) {
-        const int st = (stage + i) % C::STAGES;
-        if (u + i < fetched) mbar_wait(&bars[warp][st], st > stage ? parity : parity ^ 1, p.ctl, &abort_flag, 21);
-      }
+      for (int i = u + 1; i < u + C::STAGES && i < units; ++i)
+        mbar_wait(&bars[warp][i % C::STAGES], i / C::STAGES & 1, p.ctl, &abort_flag, 21);
       return;
     }
-    const int kb = meta[warp][stage];
-    if (kb >= 0) {
-      const uint8_t* rec = ring + stage * G::REC;
-      const bool edge = kb + kKvRec - 1 > p_lo || (window >= 0 && kb < p_hi - window);
-      // scores, S^T[key][query]
-      float s[2][NT][4];
-      float vs[2][2][NG];  // value scales of the keys of this lane's rows
+    const int kb0 = meta[warp][stage];
+    const int p_hi = sp.p_hi;
+    // the unit's steps: a record each, or half a record with two query column tiles (none for a unit
+    // that was not fetched)
+#pragma unroll 1
+    for (int kb = kb0; kb >= 0 && kb < kb0 + U && kb <= p_hi; kb += 16 * TL) {
+      const uint32_t rec = smem_u32(ring) + stage * C::STAGE + (kb - kb0) / kKvRec * G::REC;
+      const uint32_t tile0 = (kb - kb0) % kKvRec / 16;  // of the record; always 0 when a step is a record
+      const uint32_t kaddr = rec + tile0 * 16 * G::ROWB + gid * 4 * G::KP + c * G::KP;
+      const uint32_t saddr = rec + G::KSCALE + tile0 * 16 * 2 * NG + gid * 2 * NG;
+      const uint32_t va = rec + G::VCODES + tile0 * 16 * G::ROWB + lane * 16;
+      const bool edge = kb + 16 * TL - 1 > sp.p_lo || (window >= 0 && kb < p_hi - window);
+      // scores S^T[key][query], unscaled, and the value scales of the keys of this lane's rows
+      float x[TL][NT][4];
+      unsigned int vs[TL][2];
 #pragma unroll
-      for (int tl = 0; tl < 2; ++tl) {
+      for (int tl = 0; tl < TL; ++tl) {
+        const uint32_t ka = kaddr + tl * 16 * G::ROWB;
         unsigned int k0[KW], k1[KW];
 #pragma unroll
-        for (int x = 0; x < G::KB / G::KP; ++x) {
-          const uint8_t* at = rec + tl * 16 * G::ROWB + x * 64 * G::KP + gid * 4 * G::KP + c * G::KP;
+        for (int y = 0; y < G::KB / G::KP; ++y) {
           if (G::KP == 16) {
-            const uint4 a = lds16<NT == 2 && G::BITS == 8>(at), b = lds16<NT == 2 && G::BITS == 8>(at + 32 * G::KP);
-            k0[4 * x] = a.x, k0[4 * x + 1] = a.y, k0[4 * x + 2] = a.z, k0[4 * x + 3] = a.w;
-            k1[4 * x] = b.x, k1[4 * x + 1] = b.y, k1[4 * x + 2] = b.z, k1[4 * x + 3] = b.w;
+            lds16(ka + y * 64 * G::KP, &k0[4 * y]);
+            lds16(ka + y * 64 * G::KP + 32 * G::KP, &k1[4 * y]);
           } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(at);
-            const uint2 b = *reinterpret_cast<const uint2*>(at + 32 * G::KP);
-            k0[0] = a.x, k0[1] = a.y, k1[0] = b.x, k1[1] = b.y;
+            lds8(ka, k0);
+            lds8(ka + 32 * G::KP, k1);
           }
         }
         float sc[NG][NT][4];
 #pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            sc[g][nt][0] = sc[g][nt][2] = csum[nt][g][0];
-            sc[g][nt][1] = sc[g][nt][3] = csum[nt][g][1];
-          }
-#pragma unroll
         for (int wi = 0; wi < KW; ++wi) {
           const int g = NG == 1 ? 0 : wi / 2;
-          if (G::BITS == 4) {
+          const bool first = NG == 1 ? wi == 0 : wi % 2 == 0;
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-              const unsigned int a = k0[wi] >> (8 * z), b = k1[wi] >> (8 * z);
+          for (int z = 0; z < (G::BITS == 4 ? 2 : 1); ++z) {
+            const unsigned int m0 = G::BITS == 4 ? 0x000f000fu : 0x00ff00ffu, m1 = G::BITS == 4 ? 0x00f000f0u : m0;
+            const unsigned int a = z ? k0[wi] >> 8 : k0[wi], b = z ? k1[wi] >> 8 : k1[wi];
+            const unsigned int a2 = G::BITS == 4 ? a & m1 : k0[wi] >> 8 & m0, a3 = G::BITS == 4 ? b & m1 : k1[wi] >> 8 & m0;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16(sc[g][nt], a & 0x000f000fu, b & 0x000f000fu, a & 0x00f000f0u, b & 0x00f000f0u,
-                        qb[nt][2 * wi + z][0], qb[nt][2 * wi + z][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              const unsigned int(&qf)[2] = qb[nt][G::BITS == 4 ? 2 * wi + z : wi];
+              if (first && z == 0) mma_f16(sc[g][nt], a & m0, b & m0, a2, a3, qf, csum[nt][g][0], csum[nt][g][1]);
+              else mma_f16(sc[g][nt], a & m0, b & m0, a2, a3, qf);
             }
-          } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(sc[g][nt], k0[wi] & 0x00ff00ffu, k1[wi] & 0x00ff00ffu, (k0[wi] >> 8) & 0x00ff00ffu,
-                      (k1[wi] >> 8) & 0x00ff00ffu, qb[nt][wi][0], qb[nt][wi][1]);
           }
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int i = tl * 16 + gid + 8 * hf;
+          const uint32_t sa = saddr + (tl * 16 + 8 * hf) * 2 * NG;
           float ks[NG];
           if (NG == 2) {
-            const unsigned int a = *reinterpret_cast<const unsigned int*>(rec + G::KSCALE + i * 4);
-            const unsigned int b = *reinterpret_cast<const unsigned int*>(rec + G::VSCALE + i * 4);
+            const unsigned int a = lds4(sa);
             ks[0] = bf16_lo(a), ks[NG - 1] = bf16_hi(a);
-            vs[tl][hf][0] = bf16_lo(b), vs[tl][hf][NG - 1] = bf16_hi(b);
+            vs[tl][hf] = lds4(sa + G::VSCALE - G::KSCALE);
           } else {
-            ks[0] = bf16_bits(*reinterpret_cast<const unsigned short*>(rec + G::KSCALE + i * 2));
-            vs[tl][hf][0] = bf16_bits(*reinterpret_cast<const unsigned short*>(rec + G::VSCALE + i * 2));
+            ks[0] = bf16_bits(lds2(sa));
+            vs[tl][hf] = lds2(sa + G::VSCALE - G::KSCALE);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              float x = sc[0][nt][2 * hf + q] * ks[0];
-              if (NG == 2) x = fmaf(sc[NG - 1][nt][2 * hf + q], ks[NG - 1], x);
-              s[tl][nt][2 * hf + q] = x * qmul[nt][q];
+              float v = sc[0][nt][2 * hf + q] * ks[0];
+              if (NG == 2) v = fmaf(sc[NG - 1][nt][2 * hf + q], ks[NG - 1], v);
+              x[tl][nt][2 * hf + q] = v;
             }
         }
       }
       if (edge) {  // masked pairs get -inf; a key that no row of the tile sees also loses its value scale
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
+        for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int key = kb + tl * 16 + gid + 8 * hf;
-            if (key > p_hi || (window >= 0 && key < p_lo - window))
-#pragma unroll
-              for (int g = 0; g < NG; ++g) vs[tl][hf][g] = 0.f;
+            if (key > p_hi || (window >= 0 && key < sp.p_lo - window)) vs[tl][hf] = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int q = 0; q < 2; ++q)
-                if (key > pcol[nt][q] || (window >= 0 && key < pcol[nt][q] - window))
-                  s[tl][nt][2 * hf + q] = -INFINITY;
+              {
+                const int pos = s_pos[warp][nt * 8 + 2 * c + q];
+                if (key > pos || (window >= 0 && key < pos - window)) x[tl][nt][2 * hf + q] = -INFINITY;
+              }
           }
       }
       // The running maximum may lag by 8 (a factor 256 in p), and the values' unit is a power of two
-      // at or above every scale seen: both move seldom, so the usual record costs one vote here.
-      bool move = false;
+      // at or above every scale seen: both move seldom, so the usual step costs one vote here.
+      float xm[NT][2];
+      __nv_bfloat162 vm2 = *reinterpret_cast<const __nv_bfloat162*>(&vs[0][0]);
 #pragma unroll
-      for (int tl = 0; tl < 2; ++tl)
+      for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
+          vm2 = __hmax2(vm2, *reinterpret_cast<const __nv_bfloat162*>(&vs[tl][hf]));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) move |= s[tl][nt][2 * hf + q] > m[nt][q] + 8.f;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) move |= vs[tl][hf][g] > vref;
+            for (int q = 0; q < 2; ++q)
+              xm[nt][q] = tl == 0 && hf == 0 ? x[0][nt][q] : fmaxf(xm[nt][q], x[tl][nt][2 * hf + q]);
         }
+      float vm = fmaxf(__low2float(vm2), __high2float(vm2));
+      bool move = vm > vref;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) move |= fmaf(xm[nt][q], qmul[nt][q], -m[nt][q]) > 8.f;
       if (__any_sync(0xffffffffu, move)) {
-        float vm = 0.f;
-#pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-            for (int g = 0; g < NG; ++g) vm = fmaxf(vm, vs[tl][hf][g]);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
         float fv = 1.f;
@@ -597,138 +612,146 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
           float f[2];
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
-            float mx = m[nt][q];
-#pragma unroll
-            for (int tl = 0; tl < 2; ++tl) mx = fmaxf(mx, fmaxf(s[tl][nt][q], s[tl][nt][2 + q]));
+            float mx = xm[nt][q];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            mx = fmaxf(m[nt][q], mx * qmul[nt][q]);
             f[q] = m[nt][q] == mx ? 1.f : ex2_approx(m[nt][q] - mx);
             m[nt][q] = mx;
             l[nt][q] *= f[q];
             f[q] *= fv;
           }
 #pragma unroll
-          for (int x = 0; x < MT; ++x)
+          for (int y = 0; y < MT; ++y)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[nt][x][i] *= f[i & 1];
+            for (int i = 0; i < 4; ++i) acc[nt][y][i] *= f[i & 1];
         }
       }
       // probabilities, and times the value scale as the fp16 operand P^T[key][query]
       const float vinv = vref > 0.f ? 64.f / vref : 0.f;
-      unsigned int pb[2][NG][NT][2];
+      unsigned int pb[TL][NG][NT][2];
 #pragma unroll
-      for (int tl = 0; tl < 2; ++tl)
+      for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
+        for (int hf = 0; hf < 2; ++hf) {
+          float sv[NG];
+          sv[0] = bf16_lo(vs[tl][hf]) * vinv;
+          if (NG == 2) sv[NG - 1] = bf16_hi(vs[tl][hf]) * vinv;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float pr[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float ref = m[nt][q] == -INFINITY ? 0.f : m[nt][q];
-              pr[q] = ex2_approx(s[tl][nt][2 * hf + q] - ref);
+              pr[q] = ex2_approx(fmaf(x[tl][nt][2 * hf + q], qmul[nt][q], -m[nt][q]));
               l[nt][q] += pr[q];
             }
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
-              const float sv = vs[tl][hf][g] * vinv;
-              float w0 = pr[0] * sv, w1 = pr[1] * sv;
+              float w0 = pr[0] * sv[g], w1 = pr[1] * sv[g];
               if (edge) {
-                if (s[tl][nt][2 * hf] == -INFINITY) w0 = 0.f;
-                if (s[tl][nt][2 * hf + 1] == -INFINITY) w1 = 0.f;
+                if (x[tl][nt][2 * hf] == -INFINITY) w0 = 0.f;
+                if (x[tl][nt][2 * hf + 1] == -INFINITY) w1 = 0.f;
               }
               pb[tl][g][nt][hf] = transpose8(pack_h2(w0, w1));
             }
           }
-      // O^T[dim][query] of this record, started at the zero point's share
-      float corr[NG][NT][4];
-      constexpr unsigned int NZ = 0x80008000u | G::Z | (G::Z << 16);
-#pragma unroll
-      for (int g = 0; g < NG; ++g)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) corr[g][nt][i] = 0.f;
-#pragma unroll
-          for (int tl = 0; tl < 2; ++tl) mma_f16(corr[g][nt], NZ, NZ, NZ, NZ, pb[tl][g][nt][0], pb[tl][g][nt][1]);
         }
-      constexpr bool HALVES = NT == 2 && VW == 4;  // 8-byte reads, half of the words live (registers)
-      unsigned int uv[2][G::VB];
-      if (!HALVES) {
+      // O^T[dim][query] of this step, started at the zero point's share: -Z sum of the weights, from a
+      // product with a constant operand (16 times that where the codes are in bits 4..7)
+      constexpr int NZ = G::BITS == 4 ? 2 : 1;
+      // words of the record's values: [tile][slot (key of the lane)][word]
+      constexpr bool HALVES = VW == 4;  // 8-byte reads, half of the words live (registers)
+      float corr[NZ][NT][2];
+      {
+        unsigned int uv[TL][G::VB];
+        if (!HALVES) {
 #pragma unroll
-        for (int tl = 0; tl < 2; ++tl)
+          for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
-          for (int x = 0; x < G::VB / 4; ++x) {
-            const uint4 a = *reinterpret_cast<const uint4*>(rec + G::VCODES + tl * 16 * G::ROWB + x * 512 + lane * 16);
-            uv[tl][4 * x] = a.x, uv[tl][4 * x + 1] = a.y, uv[tl][4 * x + 2] = a.z, uv[tl][4 * x + 3] = a.w;
-          }
-      }
-#pragma unroll
-      for (int wj = 0; wj < VW; ++wj) {
-        const int g = NG == 1 ? 0 : wj;
-        if (HALVES && wj % 2 == 0) {
-#pragma unroll
-          for (int tl = 0; tl < 2; ++tl)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              asm volatile("ld.volatile.shared.v2.u32 {%0, %1}, [%2];"
-                           : "=r"(uv[tl][4 * x + wj]), "=r"(uv[tl][4 * x + (wj | 1)])
-                           : "r"(smem_u32(rec + G::VCODES + tl * 16 * G::ROWB + x * 512 + lane * 16 + wj * 4))
-                           : "memory");
+            for (int y = 0; y < G::VB / 4; ++y) lds16(va + tl * 16 * G::ROWB + y * 512, &uv[tl][4 * y]);
         }
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {  // low and high halves of the word: 4 or 2 dims each
-          unsigned int x01[2], x23[2];
-#pragma unroll
-          for (int tl = 0; tl < 2; ++tl) {
-            const unsigned int sel = part ? 0x7632u : 0x5410u;
-            x01[tl] = __byte_perm(uv[tl][wj], uv[tl][VW + wj], sel);
-            x23[tl] = __byte_perm(uv[tl][2 * VW + wj], uv[tl][3 * VW + wj], sel);
-          }
-#pragma unroll
-          for (int z = 0; z < (G::BITS == 4 ? 2 : 1); ++z) {
-            const unsigned int mask = G::BITS == 8 ? 0x00ff00ffu : z ? 0x00f000f0u : 0x000f000fu;
-            const int x = G::BITS == 4 ? 4 * wj + 2 * part + z : 2 * wj + part;
+        for (int wj = 0; wj < VW; ++wj) {
+          const int g = NG == 1 ? 0 : wj;
+          if (wj == 0 || NG == 2) {
+            constexpr unsigned int ZC = 0x80008000u | G::Z | (G::Z << 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               float d[4];
+              mma_f16(d, ZC, ZC, ZC, ZC, pb[0][g][nt], 0.f, 0.f);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) d[i] = z ? corr[g][nt][i] * 16.f : corr[g][nt][i];
+              for (int tl = 1; tl < TL; ++tl) mma_f16(d, ZC, ZC, ZC, ZC, pb[tl][g][nt]);
 #pragma unroll
-              for (int tl = 0; tl < 2; ++tl)
-                mma_f16(d, x01[tl] & mask, (x01[tl] >> 8) & mask, x23[tl] & mask, (x23[tl] >> 8) & mask,
-                        pb[tl][g][nt][0], pb[tl][g][nt][1]);
+              for (int z = 0; z < NZ; ++z)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[nt][x][i] += d[i];
+                for (int i = 0; i < 2; ++i) corr[z][nt][i] = z ? 16.f * d[i] : d[i];
+            }
+          }
+          if (HALVES && wj % 2 == 0) {
+#pragma unroll
+            for (int tl = 0; tl < TL; ++tl)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) lds8(va + tl * 16 * G::ROWB + y * 512 + wj * 4, &uv[tl][4 * y + wj]);
+          }
+#pragma unroll
+          for (int part = 0; part < 2; ++part) {  // low and high halves of the word: 4 or 2 dims each
+            unsigned int x01[TL], x23[TL];
+#pragma unroll
+            for (int tl = 0; tl < TL; ++tl) {
+              const unsigned int sel = part ? 0x7632u : 0x5410u;
+              x01[tl] = __byte_perm(uv[tl][wj], uv[tl][VW + wj], sel);
+              x23[tl] = __byte_perm(uv[tl][2 * VW + wj], uv[tl][3 * VW + wj], sel);
+            }
+#pragma unroll
+            for (int z = 0; z < NZ; ++z) {
+              const unsigned int mask = G::BITS == 8 ? 0x00ff00ffu : z ? 0x00f000f0u : 0x000f000fu;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float d[4];
+                mma_f16(d, x01[0] & mask, (x01[0] >> 8) & mask, x23[0] & mask, (x23[0] >> 8) & mask, pb[0][g][nt],
+                        corr[z][nt][0], corr[z][nt][1]);
+#pragma unroll
+                for (int tl = 1; tl < TL; ++tl)
+                  mma_f16(d, x01[tl] & mask, (x01[tl] >> 8) & mask, x23[tl] & mask, (x23[tl] >> 8) & mask, pb[tl][g][nt]);
+                float(&o)[4] = acc[nt][G::BITS == 4 ? 4 * wj + 2 * part + z : 2 * wj + part];
+                const float2 s0 = fadd2(make_float2(o[0], o[1]), make_float2(d[0], d[1]));
+                const float2 s1 = fadd2(make_float2(o[2], o[3]), make_float2(d[2], d[3]));
+                o[0] = s0.x, o[1] = s0.y, o[2] = s1.x, o[3] = s1.y;
+              }
             }
           }
         }
       }
-    } else if (kb == -2) {  // a block number out of range: the rows become NaN
+    }
+    if (kb0 == -2) {  // a block number out of range: the rows become NaN
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int q = 0; q < 2; ++q) l[nt][q] = __uint_as_float(0x7fc00000u);
     }
     __syncwarp();
-    fetch(stage);
+    fetch(u + C::STAGES);
     __syncwarp();
-    if (++stage == C::STAGES) stage = 0, parity ^= 1;
     const bool last = j == s_ent[warp].nrec - 1;
     if (last || u == units - 1) finish();
     ++j;
     if (last && u + 1 < units) {
       j = 0;
-      if (++h == p.Hkv) {
+      int e = sp.e, h = sp.h + 1;
+      const bool turn = h == p.Hkv;
+      if (turn) {
         h = 0;
         do {
           ++e;
         } while (pre[e + 1] == pre[e]);
-        __syncwarp();
-        const KvEntry t = kv_entry<SPARSE>(p, e, RT, false);
-        if (lane == 0) s_ent[warp] = t;
-        __syncwarp();
       }
+      __syncwarp();
+      if (turn) {
+        const KvEntry t = kv_entry<SPARSE>(p, e, RT, U, false);
+        if (lane == 0) s_ent[warp] = t;
+      }
+      if (lane == 0) sp.e = e, sp.h = h;
+      __syncwarp();
       begin();
     }
   }
@@ -736,7 +759,7 @@ __global__ void __launch_bounds__(kAttendWarps * 32, AttendCfg<G, NT>::CTAS) kv_
 
 // Units before each entry when there are more entries than a CTA scans by itself: one CTA.
 template <bool SPARSE>
-__global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT) {
+__global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT, int U) {
   __shared__ long long s_warp[8];
   pdl_wait();
   pdl_trigger();
@@ -744,7 +767,7 @@ __global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT) {
   long long run = 0;
   for (int e0 = 0; e0 < p.E; e0 += 256) {
     const int e = e0 + tid;
-    long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, true).nrec : 0;
+    long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, U, true).nrec : 0;
     const long long own = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -765,72 +788,88 @@ __global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT) {
 }
 
 // Joins the parts of a query row that was cut between workers (one CTA a row), in the workers' order,
-// and writes the rows that see no key: o = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max).
+// and writes the rows that see no key: o = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max).  A chain
+// of loads, so each step's loads are issued together: the row's place from the batch's own arrays
+// before the parts are waited for, then each warp's parts with their logsumexps in one pass.
 constexpr int kJoinThreads = 256;
 template <int HD, bool SPARSE>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int max_workers) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int U, int max_workers) {
   constexpr int V = HD / 32;  // dims of a lane
-  __shared__ float s_red[8];
-  __shared__ float s_o[8][HD];
-  pdl_wait();
-  pdl_trigger();
-  if (SPARSE && blockIdx.x == 0) kv_report_bad(p.rows, p.ctl, 9);
+  constexpr int W = kJoinThreads / 32;
+  __shared__ float s_m[W], s_l[W];
+  __shared__ float s_o[W][HD];
   const int n = blockIdx.x % p.RV;
   const long long seg = blockIdx.x / p.RV;
   const int e = (int)(seg / p.Hkv), h = (int)(seg - (long long)e * p.Hkv);
-  const long long first = p.prefix[e], nrec = p.prefix[e + 1] - first, total = p.prefix[p.E] * p.Hkv;
-  const long long workers = min((long long)max_workers, total);
+  // the batch's arrays are older than the kernel before this one, which has waited for them
+  const KvEntry t = kv_entry<SPARSE>(p, e, RT, U, false);
+  pdl_wait();
+  pdl_trigger();
+  if (SPARSE && blockIdx.x == 0) kv_report_bad(p.rows, p.ctl, 9);
+  if (n >= t.nrows) return;
   long long w0 = 0, w1 = -1;
-  if (nrec > 0) {
-    const long long f0 = first * p.Hkv + h * nrec;
+  if (t.nrec > 0) {
+    const long long first = p.prefix[e], total = p.prefix[p.E] * p.Hkv;
+    const long long workers = min((long long)max_workers, total);
+    const long long f0 = first * p.Hkv + (long long)h * t.nrec;
     w0 = worker_of(f0, total, workers);
-    w1 = worker_of(f0 + nrec - 1, total, workers);
+    w1 = worker_of(f0 + t.nrec - 1, total, workers);
     if (w0 == w1) return;  // one worker had all of it
   }
-  const KvEntry t = kv_entry<SPARSE>(p, e, RT, false);
-  if (n >= t.nrows) return;
   const int rho = t.rho0 + n;
   const long long qrow = (long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // the first worker's part is its last (slot 1), the others' their first (slot 0)
-  auto part = [&](long long w) { return (w * 2 + (w == w0 ? 1 : 0)) * p.RV + n; };
-  float mx = -INFINITY;
-  for (long long w = w0 + tid; w <= w1; w += kJoinThreads) mx = fmaxf(mx, p.part_lse[part(w)]);
+  float acc[V], sum = 0.f, mx = -INFINITY;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if (lane == 0) s_red[warp] = mx;
-  __syncthreads();
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (long long w = w0 + warp; w <= w1; w += 4 * W) {
+    float ls[4], v[4][V];
 #pragma unroll
-  for (int x = 0; x < 8; ++x) mx = fmaxf(mx, s_red[x]);
-  const float ref = mx == -INFINITY ? 0.f : mx;
-  float acc[V], sum = 0.f;
+    for (int k = 0; k < 4; ++k) {
+      const long long wk = w + k * W;
+      const bool live = wk <= w1;
+      // the first worker's part is its last (slot 1), the others' their first (slot 0)
+      const long long r = (wk * 2 + (wk == w0 ? 1 : 0)) * p.RV + n;
+      ls[k] = live ? p.part_lse[r] : -INFINITY;
+      const float* src = p.part_o + r * HD + lane * V;
 #pragma unroll
-  for (int x = 0; x < V; ++x) acc[x] = 0.f;
-#pragma unroll 4
-  for (long long w = w0 + warp; w <= w1; w += 8) {
-    const long long r = part(w);
-    const float g = ex2_approx(p.part_lse[r] - ref);
-    const float* src = p.part_o + r * HD + lane * V;
-    sum += g;
-    if (V == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      acc[0] += g * v.x, acc[1] += g * v.y, acc[V - 2] += g * v.z, acc[V - 1] += g * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      acc[0] += g * v.x, acc[1] += g * v.y;
+      for (int i = 0; i < V; i += 2) {
+        const float2 f = live ? *reinterpret_cast<const float2*>(src + i) : make_float2(0.f, 0.f);
+        v[k][i] = f.x, v[k][i + 1] = f.y;
+      }
+    }
+    const float m4 = fmaxf(fmaxf(mx, fmaxf(ls[0], ls[1])), fmaxf(ls[2], ls[3]));
+    const float ref = m4 == -INFINITY ? 0.f : m4;
+    const float f = ex2_approx(mx - ref);
+    mx = m4;
+    sum *= f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float g = ex2_approx(ls[k] - ref);
+      sum += g;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += g * v[k][i];
     }
   }
 #pragma unroll
-  for (int x = 0; x < V; ++x) s_o[warp][lane * V + x] = acc[x];
-  __syncthreads();
-  if (lane == 0) s_red[warp] = sum;
+  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = acc[i];
+  if (lane == 0) s_m[warp] = mx, s_l[warp] = sum;
   __syncthreads();
   if (tid < HD) {
-    float total_sum = 0.f, v = 0.f;
+    float m = -INFINITY;
 #pragma unroll
-    for (int x = 0; x < 8; ++x) total_sum += s_red[x], v += s_o[x][tid];
-    p.o[qrow * HD + tid] = __float2bfloat16_rn(total_sum == 0.f ? 0.f : v / total_sum);
-    if (tid == 0 && p.lse) p.lse[qrow] = total_sum == 0.f ? -INFINITY : (ref + log2f(total_sum)) * 0.6931471805599453f;
+    for (int i = 0; i < W; ++i) m = fmaxf(m, s_m[i]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    float l = 0.f, o = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float g = ex2_approx(s_m[i] - ref);
+      l += s_l[i] * g, o += s_o[i][tid] * g;
+    }
+    p.o[qrow * HD + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
+    if (tid == 0 && p.lse) p.lse[qrow] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -878,18 +917,18 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& pl, double bytes
     attr_set[dev & 63] = true;
   }
   int grid = num_sms() * C::CTAS;
-  if (grid > kAttendMaxWorkers / kAttendWarps) grid = kAttendMaxWorkers / kAttendWarps;
+  if (grid > kAttendMaxWorkers / C::WARPS) grid = kAttendMaxWorkers / C::WARPS;
   if (a.scanned) {
     Prof prof(PK_ATTN_FWD, 0, 0, st);
-    GPTK_CUDA(launch_pdl(kv_scan_kernel<SPARSE>, dim3(1), dim3(256), 0, st, a, pl.RT));
+    GPTK_CUDA(launch_pdl(kv_scan_kernel<SPARSE>, dim3(1), dim3(256), 0, st, a, pl.RT, (int)C::U));
   }
   {
     Prof prof(PK_ATTN_FWD, flops, bytes, st);
-    GPTK_CUDA(launch_pdl(kern, dim3(grid), dim3(kAttendWarps * 32), C::SMEM, st, a));
+    GPTK_CUDA(launch_pdl(kern, dim3(grid), dim3(C::WARPS * 32), C::SMEM, st, a));
   }
   Prof prof(PK_ATTN_FWD, 0, 0, st);
   GPTK_CUDA(launch_pdl(kv_join_kernel<G::HD, SPARSE>, dim3((unsigned)(pl.E * a.Hkv * pl.RV)), dim3(kJoinThreads), 0, st,
-                       a, pl.RT, grid * kAttendWarps));
+                       a, pl.RT, (int)C::U, grid * C::WARPS));
   return ST_OK;
 }
 

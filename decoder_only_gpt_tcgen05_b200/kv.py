@@ -7,12 +7,11 @@ then ``attend``, over everything or over the blocks that ``select`` chose.  Noth
 the host, so a step can be captured into a CUDA graph and replayed with new contents."""
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 
 import torch
 
-from ._lib import KVBatchParams, KVCacheParams, call
+from ._lib import KVBatchParams, KVCacheParams, call, check, lib
 
 KV_BLOCK = 64  # tokens of a cache block
 
@@ -24,20 +23,33 @@ def tile_bytes(bits: int, head_dim: int) -> int:
     return n.value
 
 
-def _on(dev: torch.device):
-    """Launches go to the tensors' device, whichever is current."""
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-def _stream(dev):
-    return torch.cuda.current_stream(dev).cuda_stream
+def _launch(name: str, dev: torch.device, *args) -> None:
+    """The library call ``name`` with ``dev``'s current stream as its last argument, launched on ``dev``
+    whichever device is current.  A decoding step is a handful of calls of a few microseconds, so this
+    path takes the raw stream handle and enters a device guard only where it changes something."""
+    f = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if rc:
+        check(rc)
 
 
 def _check(t: torch.Tensor, name: str, dtype, dev, shape=None) -> None:
     assert t.dtype == dtype, f"{name}: {dtype} needed, got {t.dtype}"
     assert t.device == dev, f"{name}: on {t.device}, the cache is on {dev}"
     assert t.is_contiguous(), f"{name}: must be contiguous"
-    assert shape is None or tuple(t.shape) == tuple(shape), f"{name}: shape {tuple(shape)} needed, got {tuple(t.shape)}"
+    assert shape is None or t.shape == shape, f"{name}: shape {tuple(shape)} needed, got {tuple(t.shape)}"
+
+
+def _out(t, name: str, shape, dtype, dev) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _check(t, name, dtype, dev, shape)
+    return t
 
 
 class KVBatch:
@@ -85,6 +97,7 @@ class KVCache:
             _check(bounds, "bounds", torch.bfloat16, dev, (n_blocks, n_kv_head, 2, head_dim))
         self.n_blocks, self.n_kv_head, self.head_dim, self.bits = n_blocks, n_kv_head, head_dim, bits
         self.tiles, self.bounds, self.device = tiles, bounds, dev
+        self._scratch = {}
         self._c = KVCacheParams(tiles.data_ptr(), bounds.data_ptr() if bounds is not None else None, n_blocks,
                                 n_kv_head, head_dim, bits)
         self._ref = C.byref(self._c)
@@ -98,22 +111,19 @@ class KVCache:
         assert batch.device == self.device, "batch: on another device than the cache"
         if q is None:
             q = torch.empty((M, n_head * self.head_dim), dtype=torch.bfloat16, device=self.device)
-        _check(q, "q", torch.bfloat16, self.device, (M, n_head * self.head_dim))
-        with _on(self.device):
-            call("gpt_op_kv_append", self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope), int(qk_norm),
-                 rope_base, eps, q.data_ptr(), _stream(self.device))
+        else:
+            _check(q, "q", torch.bfloat16, self.device, (M, n_head * self.head_dim))
+        _launch("gpt_op_kv_append", self.device, self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope),
+                int(qk_norm), rope_base, eps, q.data_ptr())
         return q
 
     def read(self, batch: KVBatch, M: int, *, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
         """(k, v): bf16 [M, n_kv_head, head_dim], the values cached at the batch's new positions."""
         shape = (M, self.n_kv_head, self.head_dim)
         assert batch.device == self.device, "batch: on another device than the cache"
-        k = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if k is None else k
-        v = torch.empty(shape, dtype=torch.bfloat16, device=self.device) if v is None else v
-        _check(k, "k", torch.bfloat16, self.device, shape)
-        _check(v, "v", torch.bfloat16, self.device, shape)
-        with _on(self.device):
-            call("gpt_op_kv_read", self._ref, batch._ref, M, k.data_ptr(), v.data_ptr(), _stream(self.device))
+        k = _out(k, "k", shape, torch.bfloat16, self.device)
+        v = _out(v, "v", shape, torch.bfloat16, self.device)
+        _launch("gpt_op_kv_read", self.device, self._ref, batch._ref, M, k.data_ptr(), v.data_ptr())
         return k, v
 
     def _heads(self, q: torch.Tensor) -> int:
@@ -129,19 +139,21 @@ class KVCache:
         _check(q, "q", torch.bfloat16, self.device)
         assert batch.device == self.device, "batch: on another device than the cache"
         shapes = (M, self.n_kv_head, n_select), (M, self.n_kv_head, batch.block_table.shape[1])
-        blocks = torch.empty(shapes[0], dtype=torch.int32, device=self.device) if blocks is None else blocks
-        scores = torch.empty(shapes[1], dtype=torch.float32, device=self.device) if scores is None else scores
-        _check(blocks, "blocks", torch.int32, self.device, shapes[0])
-        _check(scores, "scores", torch.float32, self.device, shapes[1])
-        with _on(self.device):
-            call("gpt_op_kv_select", self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
-                 blocks.data_ptr(), scores.data_ptr(), _stream(self.device))
+        blocks = _out(blocks, "blocks", shapes[0], torch.int32, self.device)
+        scores = _out(scores, "scores", shapes[1], torch.float32, self.device)
+        _launch("gpt_op_kv_select", self.device, self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
+                blocks.data_ptr(), scores.data_ptr())
         return blocks, scores
 
     def scratch_bytes(self, batch: KVBatch, M: int, n_head: int, n_sel: int = 0) -> int:
-        n = C.c_size_t()
-        call("gpt_op_attention_kv_scratch_size", self._ref, batch._ref, M, n_head, n_sel, C.byref(n))
-        return n.value
+        """Bytes of scratch that attend needs; it goes by the sizes alone, so it is asked for once a size."""
+        key = (batch.n_seq, batch.max_new, batch.cu_new is None, M, n_head, n_sel > 0)
+        n = self._scratch.get(key)
+        if n is None:
+            out = C.c_size_t()
+            call("gpt_op_attention_kv_scratch_size", self._ref, batch._ref, M, n_head, n_sel, C.byref(out))
+            n = self._scratch[key] = out.value
+        return n
 
     def attend(self, batch: KVBatch, q: torch.Tensor, *, window: int = -1, blocks: torch.Tensor | None = None,
                o: torch.Tensor | None = None, lse: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
@@ -156,15 +168,13 @@ class KVCache:
             n_sel = blocks.shape[-1]
             _check(blocks, "blocks", torch.int32, self.device, (M, self.n_kv_head, n_sel))
             assert n_sel > 0, "blocks: at least one entry a list"
-        o = torch.empty_like(q) if o is None else o
-        lse = torch.empty((M, H), dtype=torch.float32, device=self.device) if lse is None else lse
-        _check(o, "o", torch.bfloat16, self.device, (M, H * self.head_dim))
-        _check(lse, "lse", torch.float32, self.device, (M, H))
+        o = _out(o, "o", (M, H * self.head_dim), torch.bfloat16, self.device)
+        lse = _out(lse, "lse", (M, H), torch.float32, self.device)
         if scratch is None:
             scratch = torch.empty(self.scratch_bytes(batch, M, H, n_sel), dtype=torch.uint8, device=self.device)
-        _check(scratch, "scratch", torch.uint8, self.device)
-        with _on(self.device):
-            call("gpt_op_attention_kv", self._ref, batch._ref, q.data_ptr(), M, H, int(window),
-                 blocks.data_ptr() if blocks is not None else None, n_sel, o.data_ptr(), lse.data_ptr(),
-                 scratch.data_ptr(), scratch.numel(), _stream(self.device))
+        else:
+            _check(scratch, "scratch", torch.uint8, self.device)
+        _launch("gpt_op_attention_kv", self.device, self._ref, batch._ref, q.data_ptr(), M, H, int(window),
+                blocks.data_ptr() if blocks is not None else None, n_sel, o.data_ptr(), lse.data_ptr(),
+                scratch.data_ptr(), scratch.numel())
         return o, lse
