@@ -110,13 +110,13 @@ __device__ __forceinline__ long long worker_of(long long f, long long total, lon
   return ((f + 1) * workers - 1) / total;
 }
 
-// d = A B + (c0, c1, c0, c1): the accumulator's start is the same in both row halves
+// d = A B + c
 __device__ __forceinline__ void mma_f16(float (&d)[4], unsigned int a0, unsigned int a1, unsigned int a2,
-                                        unsigned int a3, const unsigned int (&b)[2], float c0, float c1) {
+                                        unsigned int a3, const unsigned int (&b)[2], const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, "
-      "%10, %11};"
+      "%12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c0), "f"(c1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b[0]), "r"(b[1]), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 // d += A B
 __device__ __forceinline__ void mma_f16(float (&d)[4], unsigned int a0, unsigned int a1, unsigned int a2,
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   // ---- state of one (entry, head)
   const int window = SPARSE ? -1 : p.window;
   unsigned int qb[NT][MT][2];
-  float csum[NT][NG][2], qmul[NT][2];  // accumulator start (-Z sum q), and q's scale times log2(e) / sqrt(hd)
-  float acc[NT][MT][4], m[NT][2], l[NT][2], vref = 0.f;  // vref: power of two, the values' unit
+  float csum[NT][NG][4], qmul[NT][2];  // accumulator start (-Z sum q), and q's scale times log2(e) / sqrt(hd)
+  float acc[NT][MT][4], m[NT][2], l[NT][2], vinv;  // vinv: 64 / (the values' unit), a power of two
   auto begin = [&]() {
     const KvEntry t = s_ent[warp];
     if (lane == 0) {
@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], 2);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          csum[nt][g][i] = __shfl_sync(0xffffffffu, sum[g], (2 * c + i) * 4) * (-G::Z * 5.9604644775390625e-8f);
+          csum[nt][g][i] = csum[nt][g][2 + i] =
+              __shfl_sync(0xffffffffu, sum[g], (2 * c + i) * 4) * (-G::Z * 5.9604644775390625e-8f);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
@@ -418,7 +419,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[nt][i][k] = 0.f;
     }
-    vref = 0.f;
+    vinv = exp2i(126);
   };
 
   // ---- end of one (entry, head) in this worker: the output, or this worker's part of it
@@ -435,8 +436,8 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         const int n = nt * 8 + 2 * c + i;
         const long long qrow = s_row[warp][n];
         if (qrow >= 0) {
-          // acc is in units of 2^-24 vref / 64; the rows of bits 4..7 in 16 times that
-          const float f = sum == 0.f ? 0.f : 262144.f * vref / sum;
+          // acc is in units of 2^-24 / vinv; the rows of bits 4..7 in 16 times that
+          const float f = sum == 0.f ? 0.f : 16777216.f / sum, fi = 1.f / vinv;
           const float lse2 = sum == 0.f ? -INFINITY : m[nt][i] + log2f(sum);
 #pragma unroll
           for (int wj = 0; wj < HD / 64; ++wj) {
@@ -444,16 +445,16 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
             if (G::BITS == 4) {
 #pragma unroll
               for (int x = 0; x < 2; ++x) {
-                v[4 * x] = acc[nt][4 * wj + 2 * x][i] * f;
-                v[4 * x + 2] = acc[nt][4 * wj + 2 * x][2 + i] * f;
-                v[4 * x + 1] = acc[nt][4 * wj + 2 * x + 1][i] * (f * 0.0625f);
-                v[4 * x + 3] = acc[nt][4 * wj + 2 * x + 1][2 + i] * (f * 0.0625f);
+                v[4 * x] = acc[nt][4 * wj + 2 * x][i] * f * fi;
+                v[4 * x + 2] = acc[nt][4 * wj + 2 * x][2 + i] * f * fi;
+                v[4 * x + 1] = acc[nt][4 * wj + 2 * x + 1][i] * (f * 0.0625f) * fi;
+                v[4 * x + 3] = acc[nt][4 * wj + 2 * x + 1][2 + i] * (f * 0.0625f) * fi;
               }
             } else {
 #pragma unroll
               for (int x = 0; x < 4; ++x) {
-                v[2 * x] = acc[nt][4 * wj + x][i] * f;
-                v[2 * x + 1] = acc[nt][4 * wj + x][2 + i] * f;
+                v[2 * x] = acc[nt][4 * wj + x][i] * f * fi;
+                v[2 * x + 1] = acc[nt][4 * wj + x][2 + i] * f * fi;
               }
             }
             if (whole) {
@@ -495,9 +496,11 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
     // the unit's steps: a record each, or half a record with two query column tiles (none for a unit
     // that was not fetched)
 #pragma unroll 1
-    for (int kb = kb0; kb >= 0 && kb < kb0 + U && kb <= p_hi; kb += 16 * TL) {
-      const uint32_t rec = smem_u32(ring) + stage * C::STAGE + (kb - kb0) / kKvRec * G::REC;
-      const uint32_t tile0 = (kb - kb0) % kKvRec / 16;  // of the record; always 0 when a step is a record
+    for (int st = 0; st < (kb0 < 0 ? 0 : U / (16 * TL)); ++st) {
+      const int kb = kb0 + st * 16 * TL;
+      if (kb > p_hi) break;
+      const uint32_t rec = smem_u32(ring) + stage * C::STAGE + st * TL / 2 * G::REC;
+      const uint32_t tile0 = st * TL % 2;  // of the record; always 0 when a step is a record
       const uint32_t kaddr = rec + tile0 * 16 * G::ROWB + gid * 4 * G::KP + c * G::KP;
       const uint32_t saddr = rec + G::KSCALE + tile0 * 16 * 2 * NG + gid * 2 * NG;
       const uint32_t va = rec + G::VCODES + tile0 * 16 * G::ROWB + lane * 16;
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const unsigned int(&qf)[2] = qb[nt][G::BITS == 4 ? 2 * wi + z : wi];
-              if (first && z == 0) mma_f16(sc[g][nt], a & m0, b & m0, a2, a3, qf, csum[nt][g][0], csum[nt][g][1]);
+              if (first && z == 0) mma_f16(sc[g][nt], a & m0, b & m0, a2, a3, qf, csum[nt][g]);
               else mma_f16(sc[g][nt], a & m0, b & m0, a2, a3, qf);
             }
           }
@@ -592,7 +595,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
               xm[nt][q] = tl == 0 && hf == 0 ? x[0][nt][q] : fmaxf(xm[nt][q], x[tl][nt][2 * hf + q]);
         }
       float vm = fmaxf(__low2float(vm2), __high2float(vm2));
-      bool move = vm > vref;
+      bool move = vm * vinv > 64.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -601,11 +604,10 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
         float fv = 1.f;
-        if (vm > vref) {
-          const int ex = min((int)(__float_as_uint(vm) >> 23) - 126, 126);
-          const float nv = exp2i(max(ex, -125));
-          fv = vref / nv;
-          vref = nv;
+        if (vm * vinv > 64.f) {  // the unit becomes the power of two above vm
+          const float nv = exp2i(max(6 - ((int)(__float_as_uint(vm) >> 23) - 126), -121));
+          fv = nv / vinv;
+          vinv = nv;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -628,7 +630,6 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         }
       }
       // probabilities, and times the value scale as the fp16 operand P^T[key][query]
-      const float vinv = vref > 0.f ? 64.f / vref : 0.f;
       unsigned int pb[TL][NG][NT][2];
 #pragma unroll
       for (int tl = 0; tl < TL; ++tl)
@@ -661,7 +662,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
       constexpr int NZ = G::BITS == 4 ? 2 : 1;
       // words of the record's values: [tile][slot (key of the lane)][word]
       constexpr bool HALVES = VW == 4;  // 8-byte reads, half of the words live (registers)
-      float corr[NZ][NT][2];
+      float corr[NZ][NT][4];
       {
         unsigned int uv[TL][G::VB];
         if (!HALVES) {
@@ -677,14 +678,14 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
             constexpr unsigned int ZC = 0x80008000u | G::Z | (G::Z << 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              float d[4];
-              mma_f16(d, ZC, ZC, ZC, ZC, pb[0][g][nt], 0.f, 0.f);
+              const float zero[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16(corr[0][nt], ZC, ZC, ZC, ZC, pb[0][g][nt], zero);
 #pragma unroll
-              for (int tl = 1; tl < TL; ++tl) mma_f16(d, ZC, ZC, ZC, ZC, pb[tl][g][nt]);
+              for (int tl = 1; tl < TL; ++tl) mma_f16(corr[0][nt], ZC, ZC, ZC, ZC, pb[tl][g][nt]);
+              if (NZ == 2) {
 #pragma unroll
-              for (int z = 0; z < NZ; ++z)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) corr[z][nt][i] = z ? 16.f * d[i] : d[i];
+                for (int i = 0; i < 4; ++i) corr[NZ - 1][nt][i] = 16.f * corr[0][nt][i];
+              }
             }
           }
           if (HALVES && wj % 2 == 0) {
@@ -709,7 +710,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
               for (int nt = 0; nt < NT; ++nt) {
                 float d[4];
                 mma_f16(d, x01[0] & mask, (x01[0] >> 8) & mask, x23[0] & mask, (x23[0] >> 8) & mask, pb[0][g][nt],
-                        corr[z][nt][0], corr[z][nt][1]);
+                        corr[z][nt]);
 #pragma unroll
                 for (int tl = 1; tl < TL; ++tl)
                   mma_f16(d, x01[tl] & mask, (x01[tl] >> 8) & mask, x23[tl] & mask, (x23[tl] >> 8) & mask, pb[tl][g][nt]);
