@@ -90,12 +90,44 @@ __device__ __forceinline__ void kv_report_bad(const KvRows& r, const DevCtl& ctl
     if (!kv_seq(r, b).ok) dev_report(ctl, DEV_ERR_BAD_BATCH, site);
 }
 
+// The sequence that row m belongs to and the row's position, by a whole block at once (one round of
+// loads): into `at`; b = -1 for a row of no sequence, pos = -1 for one of a sequence out of range.
+// Ends with a barrier.
+struct KvRow {
+  int b, pos;
+};
+__device__ __forceinline__ void kv_find_row(const KvRows& r, int m, KvRow* at) {
+  if (threadIdx.x == 0) at->b = -1;
+  __syncthreads();
+  for (int b = r.cu ? threadIdx.x : m; b < r.B; b += blockDim.x) {
+    const bool mine = r.cu ? r.cu[b] <= m && m < r.cu[b + 1] : threadIdx.x == 0;
+    if (mine) {
+      const KvSeq s = kv_seq(r, b);
+      *at = KvRow{b, s.ok ? s.len - s.n + (m - s.row0) : -1};
+    }
+    if (!r.cu) break;
+  }
+  __syncthreads();
+}
+
 // cp.async.bulk: bytes (a multiple of 16) from global to this CTA's shared memory, counted on bar
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                    smem_u32(dst)),
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
+}
+
+// packed fp32 product (ffma2 and fadd2 are in ptx.cuh)
+__device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
+  uint64_t d;
+  asm("{\n\t.reg .b64 pa, pb;\n\tmov.b64 pa, {%1, %2};\n\tmov.b64 pb, {%3, %4};\n\t"
+      "mul.rn.f32x2 %0, pa, pb;\n\t}"
+      : "=l"(d)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
 }
 
 __device__ __forceinline__ float bf16_bits(unsigned int u) { return __uint_as_float(u << 16); }

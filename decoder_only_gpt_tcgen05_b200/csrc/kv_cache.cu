@@ -23,8 +23,52 @@ struct RopeFreq {
 constexpr int kAppendThreads = 256;
 
 // keeps NaN: a block whose keys hold a NaN has NaN bounds
-__device__ __forceinline__ float min_nan(float a, float b) { return (b < a || b != b) ? b : a; }
-__device__ __forceinline__ float max_nan(float a, float b) { return (b > a || b != b) ? b : a; }
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight values of one scale group to codes.  x / s is the product with an approximate reciprocal plus
+// its residual once more, which is the correctly rounded quotient: bf16 values over a bf16 scale often
+// lie exactly between two codes, and the bare product would round those either way.  Adding 1.5 2^23 + Z
+// rounds it to the integer code in the sum's low bits (one fp32 add; a float-to-int conversion has an
+// eighth of its rate).  |x / s| <= top (1 + 2^-8) rounds to at most top, so nothing is clamped.
+template <class G>
+struct Coded {
+  unsigned int w[G::BITS / 4];  // code words of the eight dims
+  float2 n[4];                  // code - Z as floats
+};
+template <class G>
+__device__ __forceinline__ Coded<G> encode8(const float2 (&x)[4], float s, float inv) {
+  Coded<G> r;
+  constexpr float MAGIC = 12582912.f + G::Z;
+  const float2 ns = make_float2(-s, -s), i2 = make_float2(inv, inv), mg = make_float2(MAGIC, MAGIC);
+  unsigned int t[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 q = fmul2(x[i], i2);
+    const float2 f = fadd2(ffma2(ffma2(q, ns, x[i]), i2, q), mg);
+    r.n[i] = fadd2(f, make_float2(-MAGIC, -MAGIC));
+    t[2 * i] = __float_as_uint(f.x), t[2 * i + 1] = __float_as_uint(f.y);
+  }
+  // the low bytes, four to a word
+  auto bytes = [](unsigned int b0, unsigned int b1, unsigned int b2, unsigned int b3) {
+    return __byte_perm(__byte_perm(b0, b1, 0x0040), __byte_perm(b2, b3, 0x0040), 0x5410);
+  };
+  if (G::BITS == 8) {
+    r.w[0] = bytes(t[0], t[1], t[2], t[3]);
+    r.w[G::BITS / 4 - 1] = bytes(t[4], t[5], t[6], t[7]);
+  } else {
+    r.w[0] = (bytes(t[0], t[2], t[4], t[6]) & 0x0f0f0f0fu) + ((bytes(t[1], t[3], t[5], t[7]) & 0x0f0f0f0fu) << 4);
+  }
+  return r;
+}
 
 template <class G>
 __global__ void __launch_bounds__(kAppendThreads)
@@ -34,7 +78,9 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
   constexpr int HD = G::HD, HALF = HD / 2;
   constexpr int LPR = HD / 16;   // lanes of a row
   constexpr int SG = 32 / LPR;   // rows of a warp
-  __shared__ float s_cos[kKvBlock][HALF], s_sin[kKvBlock][HALF];
+  // cosines and sines of a token's frequencies, in pieces of four: piece y of lane l (frequencies
+  // 8 l + 4 y ..) at y LPR + l, so that a read takes consecutive pieces
+  __shared__ float4 s_cos[kKvBlock][HALF / 4], s_sin[kKvBlock][HALF / 4];
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / blocks_per_seq;
@@ -53,144 +99,173 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
     if (threadIdx.x == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 2);
     return;
   }
-  if (rope) {
-    for (int x = threadIdx.x; x < nt * HALF; x += kAppendThreads) {
-      const int t = x / HALF, i = x - t * HALF;
-      const double a = (double)(t0 + t) * freq.f[i];
-      const float red = (float)(a - rint(a * 0.15915494309189535) * 6.283185307179586);
-      sincosf(red, &s_sin[t][i], &s_cos[t][i]);
-    }
-    __syncthreads();
-  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sg = lane / LPR, l = lane % LPR;
   const bool wide = nt >= SG;       // the groups take tokens of one head; else a head each
   const int heads = H + 2 * Hkv;
   const int hstep = wide ? 1 : SG;  // heads of a warp at a time
+  const int tstep = wide ? SG : 1;  // tokens of a warp at a time
   const long long ld = (long long)heads * HD;
   const int warps = gridDim.y * (kAppendThreads / 32);
-  for (int h0 = (blockIdx.y * (kAppendThreads / 32) + warp) * hstep; h0 < heads; h0 += warps * hstep) {
+  const __nv_bfloat16* src = qkv + (s.row0 + (t0 - pos0)) * ld + 8 * l;
+  // a (head, token) item's two octets; loaded one turn ahead, since a turn's arithmetic is about as
+  // long as the memory latency
+  auto load = [&](int h0, int tb, uint4& u, uint4& w) {
+    const int h = wide ? h0 : h0 + sg, t = wide ? tb + sg : tb;
+    const bool live = h < heads && t < nt;
+    const uint4* p = reinterpret_cast<const uint4*>(src + t * ld + (long long)h * HD);
+    u = live ? __ldg(p) : make_uint4(0, 0, 0, 0);
+    w = live ? __ldg(p + LPR) : make_uint4(0, 0, 0, 0);
+  };
+  int h0 = (blockIdx.y * (kAppendThreads / 32) + warp) * hstep;
+  uint4 u, w;
+  load(h0, 0, u, w);
+  if (rope) {
+    float* fc = reinterpret_cast<float*>(s_cos);
+    float* fs = reinterpret_cast<float*>(s_sin);
+    for (int x = threadIdx.x; x < nt * HALF; x += kAppendThreads) {
+      const int t = x / HALF, at = x - t * HALF;
+      const int i = at / 4 % LPR * 8 + at / 4 / LPR * 4 + at % 4;
+      const double a = (double)(t0 + t) * freq.f[i];
+      const float red = (float)(a - rint(a * 0.15915494309189535) * 6.283185307179586);
+      sincosf(red, fs + x, fc + x);
+    }
+    __syncthreads();
+  }
+  for (; h0 < heads; h0 += warps * hstep) {
     const int h = wide ? h0 : h0 + sg;
     const bool is_k = h >= H && h < H + Hkv, is_v = h >= H + Hkv;
+    const bool any_kv = __any_sync(0xffffffffu, h >= H), any_qk = __any_sync(0xffffffffu, !is_v);
     const int kvh = is_v ? h - H - Hkv : h - H;
+    uint8_t* head_tile = tiles + ((long long)phys * Hkv + kvh) * G::TILE;
     float mn[16], mx[16];
 #pragma unroll
     for (int x = 0; x < 16; ++x) mn[x] = INFINITY, mx[x] = -INFINITY;
-    for (int tb = 0; tb < nt; tb += wide ? SG : 1) {
+    for (int tb = 0; tb < nt; tb += tstep) {
       const int t = wide ? tb + sg : tb;
       const bool live = h < heads && t < nt;
-      const long long row = s.row0 + (t0 - pos0) + t;
-      float a[8], c[8];
+      float2 a[4], c[4];
       {
-        const uint4* p = reinterpret_cast<const uint4*>(qkv + row * ld + (long long)h * HD);
-        const uint4 u = live ? __ldg(p + l) : make_uint4(0, 0, 0, 0);
-        const uint4 w = live ? __ldg(p + LPR + l) : make_uint4(0, 0, 0, 0);
         const unsigned int uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          a[2 * x] = bf16_lo(uu[x]), a[2 * x + 1] = bf16_hi(uu[x]);
-          c[2 * x] = bf16_lo(ww[x]), c[2 * x + 1] = bf16_hi(ww[x]);
+          a[x] = make_float2(bf16_lo(uu[x]), bf16_hi(uu[x]));
+          c[x] = make_float2(bf16_lo(ww[x]), bf16_hi(ww[x]));
         }
       }
-      if (qk_norm) {
-        float ss = 0.f;
+      if (tb + tstep < nt) load(h0, tb + tstep, u, w);
+      else load(h0 + warps * hstep, 0, u, w);
+      // The norm's factor r = rsqrt(mean x^2 + eps) scales a whole row, so RoPE and the largest value
+      // are taken on the raw row (max |r x| = r max |x|) and the reductions of both run together.
+      float ss = 0.f;
+      if (qk_norm && any_qk) {
+        float2 s2 = fmul2(a[0], a[0]);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) ss += a[x] * a[x] + c[x] * c[x];
+        for (int x = 1; x < 4; ++x) s2 = ffma2(a[x], a[x], s2);
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float r = is_v ? 1.f : rsqrtf(ss / HD + eps);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) a[x] *= r, c[x] *= r;
+        for (int x = 0; x < 4; ++x) s2 = ffma2(c[x], c[x], s2);
+        ss = s2.x + s2.y;
       }
       if (rope && live && !is_v) {
 #pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const float co = s_cos[t][8 * l + x], si = s_sin[t][8 * l + x];
-          const float x1 = a[x], x2 = c[x];
-          a[x] = x1 * co - x2 * si;
-          c[x] = x1 * si + x2 * co;
+        for (int y = 0; y < 2; ++y) {
+          const float4 co = s_cos[t][y * LPR + l], si = s_sin[t][y * LPR + l];
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const float2 co2 = x ? make_float2(co.z, co.w) : make_float2(co.x, co.y);
+            const float2 si2 = x ? make_float2(si.z, si.w) : make_float2(si.x, si.y);
+            const float2 x1 = a[2 * y + x], x2 = c[2 * y + x];
+            a[2 * y + x] = ffma2(x1, co2, fmul2(x2, make_float2(-si2.x, -si2.y)));
+            c[2 * y + x] = ffma2(x1, si2, fmul2(x2, co2));
+          }
         }
       }
-      if (live && !is_k && !is_v) {
-        uint4 u, w;
-        unsigned int* uu = &u.x;
-        unsigned int* ww = &w.x;
+      float ma = 0.f, mc = 0.f;  // max |x| of each group; a NaN stays
+      if (any_kv) {
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const __nv_bfloat162 pu = __floats2bfloat162_rn(a[2 * x], a[2 * x + 1]);
-          const __nv_bfloat162 pw = __floats2bfloat162_rn(c[2 * x], c[2 * x + 1]);
+          ma = max_nan(max_nan(ma, fabsf(a[x].x)), fabsf(a[x].y));
+          mc = max_nan(max_nan(mc, fabsf(c[x].x)), fabsf(c[x].y));
+        }
+        if (G::NG == 1) ma = max_nan(ma, mc);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+          if (G::NG == 2) mc = max_nan(mc, __shfl_xor_sync(0xffffffffu, mc, o));
+        }
+      } else {
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      }
+      if (qk_norm && any_qk) {
+        const float r = is_v ? 1.f : rsqrtf(ss / HD + eps);
+        const float2 r2 = make_float2(r, r);
+        ma *= r, mc *= r;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) a[x] = fmul2(a[x], r2), c[x] = fmul2(c[x], r2);
+      }
+      if (G::NG == 1) mc = ma;
+      if (live && !is_k && !is_v) {
+        uint4 ou, ow;
+        unsigned int* uu = &ou.x;
+        unsigned int* ww = &ow.x;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const __nv_bfloat162 pu = __floats2bfloat162_rn(a[x].x, a[x].y);
+          const __nv_bfloat162 pw = __floats2bfloat162_rn(c[x].x, c[x].y);
           uu[x] = *reinterpret_cast<const unsigned int*>(&pu);
           ww[x] = *reinterpret_cast<const unsigned int*>(&pw);
         }
-        uint4* p = reinterpret_cast<uint4*>(q_out + (row * H + h) * HD);
-        p[l] = u;
-        p[LPR + l] = w;
+        uint4* p = reinterpret_cast<uint4*>(q_out + ((s.row0 + (t0 - pos0) + (long long)t) * H + h) * HD);
+        p[l] = ou;
+        p[LPR + l] = ow;
       }
-      // max |x| of each group as bits, so that an infinity or a NaN is the largest
-      unsigned int ma = 0, mc = 0;
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        ma = max(ma, __float_as_uint(a[x]) & 0x7fffffffu);
-        mc = max(mc, __float_as_uint(c[x]) & 0x7fffffffu);
-      }
-      if (G::NG == 1) ma = max(ma, mc);
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) {
-        ma = max(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-        if (G::NG == 2) mc = max(mc, __shfl_xor_sync(0xffffffffu, mc, o));
-      }
-      if (G::NG == 1) mc = ma;
       if (live && (is_k || is_v)) {
         // scale = bf16(max / TOP), and the codes are taken against the rounded scale, so its
         // rounding costs no more than the codes' own half step.  A group that holds an infinity or
         // a NaN has a NaN scale; one whose scale would be below the normal range reads as zeros.
-        float sf[2];
+        float sf[2], inv[2];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          const unsigned int m = g ? mc : ma;
-          float v = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__uint_as_float(m), (float)G::TOP)));
+          const float m = g ? mc : ma;
+          constexpr float RT = 1.f / G::TOP;
+          const float q = m * RT;  // and its residual: m / TOP correctly rounded
+          float v = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q, (float)G::TOP, m), RT, q)));
           if (v < FLT_MIN) v = 0.f;
-          if (m >= 0x7f800000u) v = __uint_as_float(0x7fc00000u);
+          if (!(m < INFINITY)) v = __uint_as_float(0x7fc00000u);
           sf[g] = v;
+          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[g]) : "f"(v));
+          if (v == 0.f) inv[g] = 0.f;
+          if (G::NG == 1) {
+            sf[1] = sf[0], inv[1] = inv[0];
+            break;
+          }
         }
-        const float ia = sf[0] > 0.f ? __fdiv_rn(1.f, sf[0]) : 0.f, ic = sf[1] > 0.f ? __fdiv_rn(1.f, sf[1]) : 0.f;
-        int na[8], nc[8];
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          // quotient, then its residual once more: bf16 values over a bf16 scale often lie exactly
-          // between two codes, and the bare product with the reciprocal would round those either way
-          const float qa = a[x] * ia, qc = c[x] * ic;
-          na[x] = min(max(__float2int_rn(fmaf(fmaf(-qa, sf[0], a[x]), ia, qa)), -G::TOP), G::TOP);
-          nc[x] = min(max(__float2int_rn(fmaf(fmaf(-qc, sf[1], c[x]), ic, qc)), -G::TOP), G::TOP);
-        }
+        const Coded<G> ca = encode8<G>(a, sf[0], inv[0]), cc = encode8<G>(c, sf[1], inv[1]);
         if (is_k && bounds != nullptr) {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float va = na[x] * sf[0], vc = nc[x] * sf[1];
-            mn[x] = min_nan(mn[x], va), mx[x] = max_nan(mx[x], va);
-            mn[8 + x] = min_nan(mn[8 + x], vc), mx[8 + x] = max_nan(mx[8 + x], vc);
+          for (int x = 0; x < 4; ++x) {
+            const float2 va = fmul2(ca.n[x], make_float2(sf[0], sf[0])), vc = fmul2(cc.n[x], make_float2(sf[1], sf[1]));
+            mn[2 * x] = min_nan(mn[2 * x], va.x), mx[2 * x] = max_nan(mx[2 * x], va.x);
+            mn[2 * x + 1] = min_nan(mn[2 * x + 1], va.y), mx[2 * x + 1] = max_nan(mx[2 * x + 1], va.y);
+            mn[8 + 2 * x] = min_nan(mn[8 + 2 * x], vc.x), mx[8 + 2 * x] = max_nan(mx[8 + 2 * x], vc.x);
+            mn[9 + 2 * x] = min_nan(mn[9 + 2 * x], vc.y), mx[9 + 2 * x] = max_nan(mx[9 + 2 * x], vc.y);
           }
         }
         const int slot = t0 + t - blk * kKvBlock, i = slot % kKvRec;
-        uint8_t* rec = tiles + ((long long)phys * Hkv + kvh) * G::TILE + (slot / kKvRec) * G::REC;
-        unsigned int wa[2] = {0, 0}, wc[2] = {0, 0};
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int at = x * G::BITS;
-          wa[at >> 5] |= (unsigned int)(na[x] + G::Z) << (at & 31);
-          wc[at >> 5] |= (unsigned int)(nc[x] + G::Z) << (at & 31);
-        }
+        uint8_t* rec = head_tile + slot / kKvRec * G::REC;
         if (is_k) {
 #pragma unroll
-          for (int w = 0; w < G::BITS / 4; ++w) {
-            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, l * (G::BITS / 4) + w)) = wa[w];
-            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, (LPR + l) * (G::BITS / 4) + w)) = wc[w];
+          for (int x = 0; x < G::BITS / 4; ++x) {
+            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, l * (G::BITS / 4) + x)) = ca.w[x];
+            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, (LPR + l) * (G::BITS / 4) + x)) = cc.w[x];
           }
         } else if (G::BITS == 4) {
-          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, l)) = wa[0];
-          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, LPR + l)) = wc[0];
+          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, l)) = ca.w[0];
+          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, LPR + l)) = cc.w[0];
         } else {
-          *reinterpret_cast<uint2*>(rec + G::value_octet(i, l)) = make_uint2(wa[0], wa[1]);
-          *reinterpret_cast<uint2*>(rec + G::value_octet(i, LPR + l)) = make_uint2(wc[0], wc[1]);
+          *reinterpret_cast<uint2*>(rec + G::value_octet(i, l)) = make_uint2(ca.w[0], ca.w[G::BITS / 4 - 1]);
+          *reinterpret_cast<uint2*>(rec + G::value_octet(i, LPR + l)) = make_uint2(cc.w[0], cc.w[G::BITS / 4 - 1]);
         }
         if (l < G::NG) {
           __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(rec + (is_k ? G::KSCALE : G::VSCALE));
@@ -217,23 +292,23 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             uint4* p = reinterpret_cast<uint4*>(bp) + l + hf * LPR;
-            uint4 u = join ? *p : make_uint4(0, 0, 0, 0);
-            unsigned int* uu = &u.x;
+            uint4 bu = join ? *p : make_uint4(0, 0, 0, 0);
+            unsigned int* uu = &bu.x;
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               float v[2];
 #pragma unroll
               for (int y = 0; y < 2; ++y) {
                 const float old = y ? bf16_hi(uu[x]) : bf16_lo(uu[x]);
-                const float w = (q ? mx : mn)[8 * hf + 2 * x + y];
-                v[y] = !join ? w : q ? max_nan(old, w) : min_nan(old, w);
+                const float f = (q ? mx : mn)[8 * hf + 2 * x + y];
+                v[y] = !join ? f : q ? max_nan(old, f) : min_nan(old, f);
               }
               // rounded outward, so that they stay bounds
               const __nv_bfloat16 e0 = q ? __float2bfloat16_ru(v[0]) : __float2bfloat16_rd(v[0]);
               const __nv_bfloat16 e1 = q ? __float2bfloat16_ru(v[1]) : __float2bfloat16_rd(v[1]);
               uu[x] = (unsigned int)__bfloat16_as_ushort(e0) | ((unsigned int)__bfloat16_as_ushort(e1) << 16);
             }
-            *p = u;
+            *p = bu;
           }
         }
       }
@@ -243,111 +318,110 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
 
 // ------------------------------------------------------------------ read
 //
-// One warp takes 16 tokens of one kv head: the same 8- or 16-byte pieces per lane that the attention
-// kernel reads, straight from global memory, each turned into rows of bf16 values (64 to 128
-// contiguous bytes a store instruction and token).
+// One CTA takes a cache block of a sequence, one warp a kv head, 16 tokens at a time: the same 8- or
+// 16-byte pieces per lane that the attention kernel reads, straight from global memory, each turned
+// into rows of bf16 values (64 to 128 contiguous bytes a store instruction and token).  A code becomes
+// a float by setting it into the low bits of 2^23.
 template <class G>
 __global__ void __launch_bounds__(256)
-kv_read_kernel(KvRows rows, int tiles_per_seq, const uint8_t* __restrict__ tiles, int n_blocks, int Hkv,
+kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tiles, int n_blocks, int Hkv,
                __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out, DevCtl ctl) {
   constexpr int HD = G::HD;
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const int b = blockIdx.x / blocks_per_seq;
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-  const long long total = (long long)rows.B * tiles_per_seq * Hkv;
-  const long long step = (long long)gridDim.x * 8;
-  for (long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); w < total; w += step) {
-    const int h = (int)(w % Hkv);
-    const long long bt = w / Hkv;
-    const int b = (int)(bt / tiles_per_seq);
-    const KvSeq s = kv_seq(rows, b);
-    if (!s.ok) {
-      if (lane == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 3);
-      continue;
-    }
-    const int pos0 = s.len - s.n;
-    const int tile = pos0 / 16 + (int)(bt - (long long)b * tiles_per_seq);  // 16-token tile of the sequence
-    const int base = tile * 16;
-    if (base >= s.len) continue;
-    const int phys = rows.table[(long long)b * rows.W + base / kKvBlock];
-    const bool bad = phys < 0 || phys >= n_blocks;
-    if (bad && lane == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 4);
+  if (h >= Hkv) return;
+  const KvSeq s = kv_seq(rows, b);
+  if (!s.ok) {
+    if (lane == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 3);
+    return;
+  }
+  const int pos0 = s.len - s.n;
+  const int blk = pos0 / kKvBlock + (blockIdx.x - b * blocks_per_seq);
+  const int t0 = max(pos0, blk * kKvBlock), t1 = min(s.len, (blk + 1) * kKvBlock);  // positions to read
+  if (t0 >= t1) return;
+  const int phys = rows.table[(long long)b * rows.W + blk];
+  const bool bad = phys < 0 || phys >= n_blocks;
+  if (bad && lane == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 4);
+  const uint8_t* tile = tiles + ((long long)(bad ? 0 : phys) * Hkv + h) * G::TILE;
+  const long long ldo = (long long)Hkv * HD;
+  const long long out0 = ((long long)s.row0 - pos0) * ldo + (long long)h * HD;  // of position 0
+#pragma unroll 1
+  for (int base = t0 & ~15; base < t1; base += 16) {
     const int slot = base % kKvBlock, i0 = slot % kKvRec;
-    const uint8_t* rec = tiles + ((long long)(bad ? 0 : phys) * Hkv + h) * G::TILE + (slot / kKvRec) * G::REC;
-    const long long row_of = (long long)s.row0 - pos0 + base;  // row of the tile's first token
-    auto live = [&](int i) { return base + i >= pos0 && base + i < s.len; };
-    auto scale = [&](int off, int i, int g) {
-      const unsigned short u = __ldg(reinterpret_cast<const unsigned short*>(rec + off) + (i0 + i) * G::NG + g);
-      return bad ? __uint_as_float(0x7fc00000u) : bf16_bits(u);
-    };
-    auto put = [&](__nv_bfloat16* out, const unsigned int* words, float sf) {  // 8 dims
-      uint4 o;
-      unsigned int* oo = &o.x;
+    const uint8_t* rec = tile + slot / kKvRec * G::REC;
+    // every load first
+    unsigned int uv[G::VB], uk[2][G::KB / 4];
+    unsigned int sv[4], sk[2];  // scales of this lane's four values and two keys (NG of 16 bits)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int at = 2 * x * G::BITS;
-        const unsigned int two = words[at >> 5] >> (at & 31);
-        const float v0 = sf * (float)((int)(two & (2 * G::Z - 1)) - G::Z);
-        const float v1 = sf * (float)((int)((two >> G::BITS) & (2 * G::Z - 1)) - G::Z);
-        const __nv_bfloat162 p = __floats2bfloat162_rn(v0, v1);
-        oo[x] = *reinterpret_cast<const unsigned int*>(&p);
-      }
-      *reinterpret_cast<uint4*>(out) = o;
-    };
-    // values: four keys of this lane, VB bytes each
-    {
-      unsigned int u[G::VB];  // 4 VB bytes
-#pragma unroll
-      for (int p = 0; p < G::VB / 4; ++p) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16));
-        u[4 * p] = x.x, u[4 * p + 1] = x.y, u[4 * p + 2] = x.z, u[4 * p + 3] = x.w;
-      }
-#pragma unroll
-      for (int sl = 0; sl < 4; ++sl) {
-        const int i = 2 * c + (sl & 1) + 8 * (sl >> 1);
-        if (live(i)) {
-          __nv_bfloat16* out = v_out + ((row_of + i) * Hkv + h) * HD;
-#pragma unroll
-          for (int wj = 0; wj < HD / 64; ++wj)
-            put(out + 64 * wj + 8 * r, u + (sl * G::VB + wj * G::BITS) / 4, scale(G::VSCALE, i, G::NG == 1 ? 0 : wj));
-        }
-      }
+    for (int p = 0; p < G::VB / 4; ++p) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16));
+      uv[4 * p] = x.x, uv[4 * p + 1] = x.y, uv[4 * p + 2] = x.z, uv[4 * p + 3] = x.w;
     }
-    // keys: rows r and r + 8 of this lane, KB bytes each: words c, c + 4, ...
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int i = r + 8 * hf;
-      unsigned int u[G::KB / 4];
+    for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
       for (int p = 0; p < G::KB / G::KP; ++p) {
-        const uint8_t* at = rec + i0 * G::ROWB + p * 64 * G::KP + i * 4 * G::KP + c * G::KP;
+        const uint8_t* at = rec + i0 * G::ROWB + p * 64 * G::KP + (r + 8 * hf) * 4 * G::KP + c * G::KP;
         if (G::KP == 16) {
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-          u[4 * p] = x.x, u[4 * p + 1] = x.y, u[4 * p + 2] = x.z, u[4 * p + 3] = x.w;
+          uk[hf][4 * p] = x.x, uk[hf][4 * p + 1] = x.y, uk[hf][4 * p + 2] = x.z, uk[hf][4 * p + 3] = x.w;
         } else {
           const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-          u[0] = x.x, u[1] = x.y;
+          uk[hf][0] = x.x, uk[hf][1] = x.y;
         }
       }
-      if (live(i)) {
-        __nv_bfloat16* out = k_out + ((row_of + i) * Hkv + h) * HD;
-        if (G::BITS == 4) {
+    auto scales = [&](int off, int i) -> unsigned int {
+      const uint8_t* at = rec + off + (i0 + i) * 2 * G::NG;
+      return G::NG == 2 ? __ldg(reinterpret_cast<const unsigned int*>(at))
+                        : __ldg(reinterpret_cast<const unsigned short*>(at));
+    };
 #pragma unroll
-          for (int wi = 0; wi < G::KB / 4; ++wi)
-            put(out + 32 * wi + 8 * c, u + wi, scale(G::KSCALE, i, G::NG == 1 ? 0 : wi / 2));
-        } else {
-          const float sf = scale(G::KSCALE, i, 0);
+    for (int sl = 0; sl < 4; ++sl) sv[sl] = scales(G::VSCALE, 2 * c + (sl & 1) + 8 * (sl >> 1));
 #pragma unroll
-          for (int wi = 0; wi < G::KB / 4; ++wi) {
-            uint2 o;
+    for (int hf = 0; hf < 2; ++hf) sk[hf] = scales(G::KSCALE, r + 8 * hf);
+
+    auto scale = [&](unsigned int u, int g) {
+      return bad ? __uint_as_float(0x7fc00000u) : G::NG == 2 && g ? bf16_hi(u) : bf16_lo(u);
+    };
+    auto value = [&](unsigned int word, int i, float sf) {  // code i of the word
+      const unsigned int u = (word >> (i * G::BITS)) & (2 * G::Z - 1);
+      return sf * (__uint_as_float(0x4b000000u | u) - (8388608.f + G::Z));
+    };
+    auto pair = [&](unsigned int word, int i, float sf) {  // codes i and i + 1 as two bf16
+      const __nv_bfloat162 p = __floats2bfloat162_rn(value(word, i, sf), value(word, i + 1, sf));
+      return *reinterpret_cast<const unsigned int*>(&p);
+    };
+    auto octet = [&](const unsigned int* w, float sf) {
+      return G::BITS == 4 ? make_uint4(pair(w[0], 0, sf), pair(w[0], 2, sf), pair(w[0], 4, sf), pair(w[0], 6, sf))
+                          : make_uint4(pair(w[0], 0, sf), pair(w[0], 2, sf), pair(w[1], 0, sf), pair(w[1], 2, sf));
+    };
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const float v0 = sf * (float)((int)((u[wi] >> (16 * x)) & 255) - G::Z);
-              const float v1 = sf * (float)((int)((u[wi] >> (16 * x + 8)) & 255) - G::Z);
-              const __nv_bfloat162 p = __floats2bfloat162_rn(v0, v1);
-              (x ? o.y : o.x) = *reinterpret_cast<const unsigned int*>(&p);
-            }
-            *reinterpret_cast<uint2*>(out + 16 * wi + 4 * c) = o;
+    for (int sl = 0; sl < 4; ++sl) {
+      const int t = base + 2 * c + (sl & 1) + 8 * (sl >> 1);
+      if (t >= t0 && t < t1) {
+        __nv_bfloat16* out = v_out + out0 + t * ldo + 8 * r;
+#pragma unroll
+        for (int wj = 0; wj < HD / 64; ++wj)
+          *reinterpret_cast<uint4*>(out + 64 * wj) =
+              octet(uv + (sl * G::VB + wj * G::BITS) / 4, scale(sv[sl], G::NG == 1 ? 0 : wj));
+      }
+    }
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      const int t = base + r + 8 * hf;
+      if (t >= t0 && t < t1) {
+        __nv_bfloat16* out = k_out + out0 + t * ldo;
+#pragma unroll
+        for (int wi = 0; wi < G::KB / 4; ++wi) {
+          const float sf = scale(sk[hf], G::NG == 1 ? 0 : wi / 2);
+          if (G::BITS == 4) {
+            *reinterpret_cast<uint4*>(out + 32 * wi + 8 * c) = octet(&uk[hf][wi], sf);
+          } else {
+            *reinterpret_cast<uint2*>(out + 16 * wi + 4 * c) =
+                make_uint2(pair(uk[hf][wi], 0, sf), pair(uk[hf][wi], 2, sf));
           }
         }
       }
@@ -449,18 +523,18 @@ GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch,
     return set_error(ST_INVALID_ARG, "kv_read: k_out and v_out must be 16-byte aligned");
   const int Hkv = cache->n_kv_head;
   const int max_new = batch->cu_new ? batch->max_new : 1;
-  const long long tps = ((long long)max_new + 14) / 16 + 1;  // 16-token tiles that max_new tokens can touch
-  if (tps > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_read: max_new too large");
+  const long long bps = ((long long)max_new + kKvBlock - 2) / kKvBlock + 1;  // blocks that max_new tokens can touch
+  if (bps * batch->n_seq > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_read: n_seq x max_new too large");
+  const int groups = (Hkv + 7) / 8, warps = (Hkv + groups - 1) / groups;  // heads spread evenly over the CTAs
+  if (groups > 65535) return set_error(ST_UNSUPPORTED, "kv_read: too many kv heads");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Prof prof(PK_MISC, 0, (double)M * Hkv * cache->head_dim * (4 + cache->bits / 4.0), st);
   return kv_dispatch(cache, [&](auto g) -> int {
     using G = decltype(g);
-    const long long items = tps * batch->n_seq * Hkv;
-    const long long want = (items + 7) / 8, most = 8LL * num_sms();
     KvRows r = kv_rows(batch, M);
     r.max_new = max_new;
-    GPTK_CUDA(launch_pdl(kv_read_kernel<G>, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, st, r, (int)tps,
-                         static_cast<const uint8_t*>(cache->tiles), (int)cache->n_blocks, Hkv,
+    GPTK_CUDA(launch_pdl(kv_read_kernel<G>, dim3((unsigned)(bps * batch->n_seq), (unsigned)groups), dim3(32 * warps), 0,
+                         st, r, (int)bps, static_cast<const uint8_t*>(cache->tiles), (int)cache->n_blocks, Hkv,
                          static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), device_ctl()));
     return ST_OK;
   });

@@ -15,86 +15,96 @@
 namespace gptk {
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreChunk = 64;  // blocks a CTA scores (see launch)
+constexpr int kScoreChunk = 128;  // blocks a CTA scores
 
 // One CTA: one token, one kv head, kScoreChunk blocks.  Eight lanes take a block, 16-byte pieces of
-// both bounds each.  Reads 4 HD bytes a block; the fp32 -> fp64 conversions (two a dim) are the
-// busiest unit.
-template <int HD>
+// both bounds each.  Reads 4 HD bytes a block.  ONE: one query head a kv head.  Loops stay rolled
+// where they can: the CTAs are short, and fetching code that runs once costs more than it saves.  The conversions
+// to fp64 run at an eighth of the fp32 rate: one a dim where a kv head has one query head (the bound is
+// chosen first), two where several share them.
+template <int HD, bool ONE>
 __global__ void __launch_bounds__(kScoreThreads)
 kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfloat16* __restrict__ bounds,
                 int n_blocks, int G, int Hkv, float* __restrict__ scores, DevCtl ctl) {
   constexpr int NC = HD / 64;
   extern __shared__ double s_q[];  // [G][NC][8 dims of a piece][8 lanes]
+  __shared__ int s_phys[kScoreChunk];
+  __shared__ KvRow at;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0) kv_report_bad(rows, ctl, 5);
   const int m = blockIdx.x / Hkv, h = blockIdx.x - m * Hkv;
-  // the token's sequence: the last one that begins at or before row m (empty ones skipped)
-  __shared__ int s_seq;
-  if (threadIdx.x == 0) {
-    int b = m < rows.B ? m : -1;
-    if (rows.cu) {
-      int lo = 0, hi = rows.B;  // first b with cu[b + 1] > m
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (rows.cu[mid + 1] > m) hi = mid;
-        else lo = mid + 1;
-      }
-      b = lo < rows.B && rows.cu[lo] <= m ? lo : -1;
-    }
-    s_seq = b;
-  }
   for (int x = threadIdx.x; x < G * HD; x += kScoreThreads) {
     const int g = x / HD, d = x - g * HD;
     const float v = __bfloat162float(q[((long long)m * Hkv + h) * G * HD + x]);
     s_q[((g * NC + d / 64) * 8 + d % 8) * 8 + (d / 8) % 8] = (double)v;
   }
-  __syncthreads();
-  const int b = s_seq;
-  if (b < 0) return;
-  const KvSeq s = kv_seq(rows, b);
-  const int pos = s.ok ? s.len - s.n + (m - s.row0) : -1;
-  const int nb = pos < 0 ? 0 : pos / kKvBlock + 1;
-  const int l = threadIdx.x & 7;
+  kv_find_row(rows, m, &at);
+  const KvRow row = at;
+  if (row.b < 0) return;
+  const int nb = row.pos < 0 ? 0 : row.pos / kKvBlock + 1;
+  const int j0 = blockIdx.y * kScoreChunk, j1 = min(j0 + kScoreChunk, rows.W);
   float* out = scores + ((long long)m * Hkv + h) * rows.W;
-  const int j1 = min((int)(blockIdx.y + 1) * kScoreChunk, rows.W);
-  for (int jb = blockIdx.y * kScoreChunk; jb < j1; jb += kScoreThreads / 8) {
+  if (j0 >= nb) {
+    for (int j = j0 + threadIdx.x; j < j1; j += kScoreThreads) out[j] = -INFINITY;
+    return;
+  }
+  for (int j = j0 + threadIdx.x; j < j1; j += kScoreThreads) {
+    int phys = j < nb ? rows.table[(long long)row.b * rows.W + j] : 0;
+    if (phys < 0 || phys >= n_blocks) {
+      dev_report(ctl, DEV_ERR_BAD_BATCH, 6);
+      phys = -1;
+    }
+    s_phys[j - j0] = phys;
+  }
+  __syncthreads();
+  const int l = threadIdx.x & 7;
+#pragma unroll 1
+  for (int jb = j0; jb < j1; jb += kScoreThreads / 8) {
     const int j = jb + (threadIdx.x >> 3);
     const bool here = j < j1, live = here && j < nb;
-    int phys = live ? rows.table[(long long)b * rows.W + j] : 0;
-    const bool bad = phys < 0 || phys >= n_blocks;
-    if (bad) {
-      if (l == 0) dev_report(ctl, DEV_ERR_BAD_BATCH, 6);
-      phys = 0;
-    }
-    const uint4* p = reinterpret_cast<const uint4*>(bounds + ((long long)phys * Hkv + h) * 2 * HD);
+    const int phys = here ? s_phys[j - j0] : 0;
+    const uint4* p = reinterpret_cast<const uint4*>(bounds + ((long long)max(phys, 0) * Hkv + h) * 2 * HD);
     double acc = 0.0;
-    if (live) {
-      uint4 lo[NC], hi[NC];
+    uint4 lo[NC], hi[NC];
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        lo[c] = __ldg(p + c * 8 + l);
-        hi[c] = __ldg(p + HD / 8 + c * 8 + l);
+    for (int c = 0; c < NC; ++c) {
+      lo[c] = live ? __ldg(p + c * 8 + l) : make_uint4(0, 0, 0, 0);
+      hi[c] = live ? __ldg(p + HD / 8 + c * 8 + l) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      const unsigned int ul[4] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w}, uh[4] = {hi[c].x, hi[c].y, hi[c].z, hi[c].w};
+      const double* qp = s_q + c * 64 + l;
+      float a[8], e[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        a[x] = x & 1 ? bf16_hi(ul[x >> 1]) : bf16_lo(ul[x >> 1]);
+        e[x] = x & 1 ? bf16_hi(uh[x >> 1]) : bf16_lo(uh[x >> 1]);
       }
-#pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        const unsigned int ul[4] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w}, uh[4] = {hi[c].x, hi[c].y, hi[c].z, hi[c].w};
+      if (ONE) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const float a = x & 1 ? bf16_hi(ul[x >> 1]) : bf16_lo(ul[x >> 1]);
-          const float e = x & 1 ? bf16_hi(uh[x >> 1]) : bf16_lo(uh[x >> 1]);
-          for (int g = 0; g < G; ++g) {
-            const double qv = s_q[((g * NC + c) * 8 + x) * 8 + l];
-            acc = fma(qv, (double)(qv > 0.0 ? e : a), acc);
+          const double qv = qp[x * 8];
+          acc = fma(qv, (double)(qv > 0.0 ? e[x] : a[x]), acc);
+        }
+      } else {
+        double da[8], de[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) da[x] = a[x], de[x] = e[x];
+#pragma unroll 1
+        for (int g = 0; g < G; ++g) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const double qv = qp[g * HD + x * 8];
+            acc = fma(qv, qv > 0.0 ? de[x] : da[x], acc);
           }
         }
       }
     }
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (here && l == 0)
-      out[j] = !live ? -INFINITY : bad ? __uint_as_float(0x7fc00000u) : (float)acc;
+    if (here && l == 0) out[j] = !live ? -INFINITY : phys < 0 ? __uint_as_float(0x7fc00000u) : (float)acc;
   }
 }
 
@@ -102,6 +112,7 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
 // best scores until there are n.  A radix select over the scores' ordered bits (four histograms of
 // 256) finds the n-th key; one ordered pass writes the chosen indices, ascending, ties to the lower.
 constexpr int kPickThreads = 256;
+constexpr int kPickKeys = 4096;  // keys kept in shared memory (more are formed anew in each pass)
 
 __device__ __forceinline__ unsigned int pick_key(float v, int j, int nb, int n_first, int n_last) {
   if (j < n_first || j >= nb - n_last) return 0xffffffffu;
@@ -114,46 +125,35 @@ __global__ void __launch_bounds__(kPickThreads)
 kv_pick_kernel(const float* __restrict__ scores, KvRows rows, int Hkv, int n, int n_first, int n_last,
                int* __restrict__ blocks) {
   __shared__ int hist[256];
-  __shared__ int s_nb, s_bin, s_left;
+  __shared__ unsigned int s_key[kPickKeys];
+  __shared__ KvRow at;
+  __shared__ int s_bin, s_left;
   __shared__ int wsum[kPickThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int m = blockIdx.x / Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) {
-    int b = m < rows.B ? m : -1;
-    if (rows.cu) {
-      int lo = 0, hi = rows.B;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (rows.cu[mid + 1] > m) hi = mid;
-        else lo = mid + 1;
-      }
-      b = lo < rows.B && rows.cu[lo] <= m ? lo : -1;
-    }
-    int nb = -1;
-    if (b >= 0) {
-      const KvSeq s = kv_seq(rows, b);
-      nb = s.ok ? (s.len - s.n + (m - s.row0)) / kKvBlock + 1 : 0;
-    }
-    s_nb = nb;
-  }
-  __syncthreads();
-  const int nb = s_nb;
-  if (nb < 0) return;
+  kv_find_row(rows, m, &at);
+  if (at.b < 0) return;
+  const int nb = at.pos < 0 ? 0 : at.pos / kKvBlock + 1;
   const float* sc = scores + (long long)blockIdx.x * rows.W;
   int* out = blocks + (long long)blockIdx.x * n;
   if (nb <= n) {
     for (int i = tid; i < n; i += kPickThreads) out[i] = i < nb ? i : -1;
     return;
   }
+  const bool kept = nb <= kPickKeys;
+  if (kept) {
+    for (int j = tid; j < nb; j += kPickThreads) s_key[j] = pick_key(sc[j], j, nb, n_first, n_last);
+  }
+  auto key = [&](int j) { return kept ? s_key[j] : pick_key(sc[j], j, nb, n_first, n_last); };
   unsigned int prefix = 0, mask = 0;
   int left = n;  // still to be chosen among the keys that match the prefix
   for (int shift = 24; shift >= 0; shift -= 8) {
     hist[tid] = 0;
     __syncthreads();
     for (int j = tid; j < nb; j += kPickThreads) {
-      const unsigned int k = pick_key(sc[j], j, nb, n_first, n_last);
+      const unsigned int k = key(j);
       if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
     }
     __syncthreads();
@@ -186,7 +186,7 @@ kv_pick_kernel(const float* __restrict__ scores, KvRows rows, int Hkv, int n, in
   int gt = 0, eq = 0;  // before this chunk
   for (int base = 0; base < nb; base += kPickThreads) {
     const int j = base + tid;
-    const unsigned int k = j < nb ? pick_key(sc[j], j, nb, n_first, n_last) : 0u;
+    const unsigned int k = j < nb ? key(j) : 0u;
     const bool is_gt = j < nb && k > prefix, is_eq = j < nb && k == prefix;
     const unsigned int bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
     __syncthreads();
@@ -223,7 +223,7 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     return set_error(ST_INVALID_ARG, "kv_select: n_select >= 1 and n_first + n_last <= n_select are needed");
   if ((long long)M * Hkv > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_select: M x n_kv_head too large");
   const long long chunks = ((long long)batch->max_blocks + kScoreChunk - 1) / kScoreChunk;
-  if (chunks > 65535) return set_error(ST_UNSUPPORTED, "kv_select: max_blocks above 64 x 65535");
+  if (chunks > 65535) return set_error(ST_UNSUPPORTED, "kv_select: max_blocks above 128 x 65535");
   if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
   if (!q || !blocks || !scores) return set_error(ST_INVALID_ARG, "kv_select: null q, blocks or scores");
   if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(blocks) & 3) ||
@@ -239,10 +239,12 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     const size_t smem = (size_t)G * hd * 8;
     auto* bp = static_cast<const __nv_bfloat16*>(cache->bounds);
     auto* qp = static_cast<const __nv_bfloat16*>(q);
-    GPTK_CUDA(hd == 64 ? launch_pdl(kv_score_kernel<64>, grid, dim3(kScoreThreads), smem, st, qp, r, bp,
-                                    (int)cache->n_blocks, G, Hkv, scores, device_ctl())
-                       : launch_pdl(kv_score_kernel<128>, grid, dim3(kScoreThreads), smem, st, qp, r, bp,
-                                    (int)cache->n_blocks, G, Hkv, scores, device_ctl()));
+    auto go = [&](auto kern) {
+      return launch_pdl(kern, grid, dim3(kScoreThreads), smem, st, qp, r, bp, (int)cache->n_blocks, G, Hkv, scores,
+                        device_ctl());
+    };
+    GPTK_CUDA(hd == 64 ? (G == 1 ? go(kv_score_kernel<64, true>) : go(kv_score_kernel<64, false>))
+                       : (G == 1 ? go(kv_score_kernel<128, true>) : go(kv_score_kernel<128, false>)));
   }
   Prof prof(PK_MISC, 0, (double)M * Hkv * (4.0 * batch->max_blocks + 4.0 * n_select), st);
   GPTK_CUDA(launch_pdl(kv_pick_kernel, dim3((unsigned)(M * Hkv)), dim3(kPickThreads), 0, st,
