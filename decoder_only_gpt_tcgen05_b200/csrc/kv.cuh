@@ -110,14 +110,15 @@ __device__ __forceinline__ void kv_find_row(const KvRows& r, int m, KvRow* at) {
   __syncthreads();
 }
 
-// cp.async.bulk: bytes (a multiple of 16) from global to this CTA's shared memory, counted on bar
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                   smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
+// Announces `bytes` (a multiple of 16) on the mbarrier at shared address bar and copies them from
+// global memory to shared address dst (cp.async.bulk), counted on it.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .b64 st;\n\tmbarrier.arrive.expect_tx.shared::cta.b64 st, [%3], %2;\n\t"
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
 }
-
 // packed fp32 product (ffma2 and fadd2 are in ptx.cuh)
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {
   uint64_t d;

@@ -39,6 +39,7 @@ struct AttendArgs {
   const int* sel;  // [M, Hkv, n_sel] listed blocks, or null: every visible one
   KvRows rows;
   int n_blocks, H, Hkv, G, n_sel, window;
+  unsigned int block_bytes;  // of all kv heads' tiles
   int E, QT;       // entries, and tiles of query rows a sequence (sparse: a token) has
   int RV;          // query rows of a tile that can be in use (scratch rows)
   int scanned;     // 1: prefix already holds the units before each entry (E large)
@@ -139,6 +140,8 @@ __device__ __forceinline__ unsigned int pack_h2(float lo, float hi) {
 __device__ __forceinline__ float2 unpack_h2(unsigned int u) {
   return __half22float2(*reinterpret_cast<const __half2*>(&u));
 }
+// bytes 1 and 3, each in the low half of 16 bits
+__device__ __forceinline__ unsigned int odd_bytes(unsigned int x) { return __byte_perm(x, 0, 0x4341); }
 // Shared-memory reads by 32-bit address, kept where they are written: hoisted by the compiler they
 // would all be live at once, and the kernel is short of registers.
 __device__ __forceinline__ void lds16(uint32_t a, unsigned int* v) {
@@ -248,7 +251,6 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   if (w >= workers) return;
   const long long ua = w * total / workers;
   const int units = (int)((w + 1) * total / workers - ua);
-  uint8_t* ring = ring_all + warp * C::RING;
 
   // ---- the fetching iterator, C::STAGES units ahead of the computing one
   int fe, fh, fj;
@@ -266,11 +268,12 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   }
   int j = fj;  // the computing iterator's unit; its entry and head are in sp
   KvSpan& sp = s_span[warp];
-  int f_phys = 0, f_kb = 0, f_next = -1;
   const KvEntry& ft = s_fent[warp];
-  // loads the block number of unit (fe, fh, fj); `fresh`: the listed block was not loaded ahead
+  const uint32_t bar0 = smem_u32(&bars[warp][0]), ring0 = smem_u32(ring_all) + warp * C::RING;
+  int f_phys = 0, f_kb = 0, f_tab = 0, f_next = -1;
+  // the block number of unit (fe, fh, fj): after the first of a head, what changes is added up
   auto look_up = [&](bool fresh) {
-    int blk;
+    if (fresh) f_tab = ft.b * p.rows.W;
     if (SPARSE) {
       constexpr int PER = kKvBlock / U;  // units of a listed block
       if (fj % PER && !fresh) {
@@ -278,7 +281,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         return;
       }
       const int* list = p.sel + ((long long)ft.row0 * p.Hkv + fh) * p.n_sel + fj / PER;
-      blk = fresh ? list[0] : f_next;
+      const int blk = fresh ? list[0] : f_next;
       f_next = fj + PER < ft.nrec ? list[1] : -1;
       if (blk < 0 || blk >= ft.nb) {
         f_kb = -1;
@@ -286,28 +289,24 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
       }
       f_kb = blk * kKvBlock + fj % PER * U;
     } else {
-      f_kb = (ft.jlo + fj) * U;
-      blk = f_kb / kKvBlock;
+      f_kb = fresh ? (ft.jlo + fj) * U : f_kb + U;
     }
-    f_phys = p.rows.table[(long long)ft.b * p.rows.W + blk];
+    f_phys = p.rows.table[f_tab + f_kb / kKvBlock];
   };
   auto fetch = [&](int f) {  // this worker's unit f into its stage, then on to the one after it
     if (f >= units) return;
     const int stage = f % C::STAGES;
     if (lane == 0) {
-      uint64_t* bar = &bars[warp][stage];
-      if (f_kb < 0) {
-        meta[warp][stage] = -1;
-        mbar_arrive(bar);
-      } else if (f_phys < 0 || f_phys >= p.n_blocks) {
-        dev_report(p.ctl, DEV_ERR_BAD_BATCH, 8);
-        meta[warp][stage] = -2;
-        mbar_arrive(bar);
+      const uint32_t bar = bar0 + 8 * stage;
+      const bool ok = (unsigned int)f_phys < (unsigned int)p.n_blocks;
+      meta[warp][stage] = f_kb < 0 ? -1 : ok ? f_kb : -2;
+      if (f_kb >= 0 && ok) {
+        const uint8_t* src = p.tiles + (unsigned long long)f_phys * p.block_bytes +
+                             (unsigned int)(fh * G::TILE + (U == 64 ? 0 : f_kb / kKvRec % 2 * G::REC));
+        bulk_load(ring0 + stage * C::STAGE, src, C::STAGE, bar);
       } else {
-        meta[warp][stage] = f_kb;
-        mbar_expect_tx(bar, C::STAGE);
-        bulk_load(ring + stage * C::STAGE,
-                  p.tiles + ((long long)f_phys * p.Hkv + fh) * G::TILE + f_kb % kKvBlock / U * C::STAGE, C::STAGE, bar);
+        if (f_kb >= 0) dev_report(p.ctl, DEV_ERR_BAD_BATCH, 8);
+        mbar_arrive(&bars[warp][stage]);
       }
     }
     if (f + 1 >= units) return;
@@ -499,7 +498,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
     for (int st = 0; st < (kb0 < 0 ? 0 : U / (16 * TL)); ++st) {
       const int kb = kb0 + st * 16 * TL;
       if (kb > p_hi) break;
-      const uint32_t rec = smem_u32(ring) + stage * C::STAGE + st * TL / 2 * G::REC;
+      const uint32_t rec = ring0 + stage * C::STAGE + st * TL / 2 * G::REC;
       const uint32_t tile0 = st * TL % 2;  // of the record; always 0 when a step is a record
       const uint32_t kaddr = rec + tile0 * 16 * G::ROWB + gid * 4 * G::KP + c * G::KP;
       const uint32_t saddr = rec + G::KSCALE + tile0 * 16 * 2 * NG + gid * 2 * NG;
@@ -531,7 +530,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
           for (int z = 0; z < (G::BITS == 4 ? 2 : 1); ++z) {
             const unsigned int m0 = G::BITS == 4 ? 0x000f000fu : 0x00ff00ffu, m1 = G::BITS == 4 ? 0x00f000f0u : m0;
             const unsigned int a = z ? k0[wi] >> 8 : k0[wi], b = z ? k1[wi] >> 8 : k1[wi];
-            const unsigned int a2 = G::BITS == 4 ? a & m1 : k0[wi] >> 8 & m0, a3 = G::BITS == 4 ? b & m1 : k1[wi] >> 8 & m0;
+            const unsigned int a2 = G::BITS == 4 ? a & m1 : odd_bytes(k0[wi]), a3 = G::BITS == 4 ? b & m1 : odd_bytes(k1[wi]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const unsigned int(&qf)[2] = qb[nt][G::BITS == 4 ? 2 * wi + z : wi];
@@ -706,14 +705,14 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
 #pragma unroll
             for (int z = 0; z < NZ; ++z) {
               const unsigned int mask = G::BITS == 8 ? 0x00ff00ffu : z ? 0x00f000f0u : 0x000f000fu;
+              auto second = [&](unsigned int x) { return G::BITS == 8 ? odd_bytes(x) : (x >> 8) & mask; };
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float d[4];
-                mma_f16(d, x01[0] & mask, (x01[0] >> 8) & mask, x23[0] & mask, (x23[0] >> 8) & mask, pb[0][g][nt],
-                        corr[z][nt]);
+                mma_f16(d, x01[0] & mask, second(x01[0]), x23[0] & mask, second(x23[0]), pb[0][g][nt], corr[z][nt]);
 #pragma unroll
                 for (int tl = 1; tl < TL; ++tl)
-                  mma_f16(d, x01[tl] & mask, (x01[tl] >> 8) & mask, x23[tl] & mask, (x23[tl] >> 8) & mask, pb[tl][g][nt]);
+                  mma_f16(d, x01[tl] & mask, second(x01[tl]), x23[tl] & mask, second(x23[tl]), pb[tl][g][nt]);
                 float(&o)[4] = acc[nt][G::BITS == 4 ? 4 * wj + 2 * part + z : 2 * wj + part];
                 const float2 s0 = fadd2(make_float2(o[0], o[1]), make_float2(d[0], d[1]));
                 const float2 s1 = fadd2(make_float2(o[2], o[3]), make_float2(d[2], d[3]));
@@ -788,46 +787,49 @@ __global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT, int 
   if (tid == 0) p.prefix[p.E] = run;
 }
 
-// Joins the parts of a query row that was cut between workers (one CTA a row), in the workers' order,
-// and writes the rows that see no key: o = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max).  A chain
-// of loads, so each step's loads are issued together: the row's place from the batch's own arrays
-// before the parts are waited for, then each warp's parts with their logsumexps in one pass.
+// Joins the parts of the query rows that were cut between workers, in the workers' order, and writes the
+// rows that see no key: o = sum_i 2^(lse_i - max) o_i / sum_i 2^(lse_i - max).  WPR warps share a row:
+// eight where few rows are cut into many parts, one where there are many rows.  It is a chain of loads,
+// so each step's loads are issued together: the row's place from the batch's own arrays before the
+// parts are waited for, then four parts with their logsumexps at a time.
 constexpr int kJoinThreads = 256;
-template <int HD, bool SPARSE>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int U, int max_workers) {
+template <int HD, bool SPARSE, int WPR>
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int U, int max_workers, int rows) {
   constexpr int V = HD / 32;  // dims of a lane
   constexpr int W = kJoinThreads / 32;
   __shared__ float s_m[W], s_l[W];
   __shared__ float s_o[W][HD];
-  const int n = blockIdx.x % p.RV;
-  const long long seg = blockIdx.x / p.RV;
-  const int e = (int)(seg / p.Hkv), h = (int)(seg - (long long)e * p.Hkv);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
+  const int row = blockIdx.x * (W / WPR) + warp / WPR;
+  const int seg = row / p.RV, n = row - seg * p.RV;
+  const int e = seg / p.Hkv, h = seg - e * p.Hkv;
   // the batch's arrays are older than the kernel before this one, which has waited for them
-  const KvEntry t = kv_entry<SPARSE>(p, e, RT, U, false);
+  KvEntry t;
+  t.nrows = 0;
+  if (row < rows) t = kv_entry<SPARSE>(p, e, RT, U, false);
   pdl_wait();
   pdl_trigger();
   if (SPARSE && blockIdx.x == 0) kv_report_bad(p.rows, p.ctl, 9);
-  if (n >= t.nrows) return;
+  bool mine = n < t.nrows;
   long long w0 = 0, w1 = -1;
-  if (t.nrec > 0) {
+  if (mine && t.nrec > 0) {
     const long long first = p.prefix[e], total = p.prefix[p.E] * p.Hkv;
     const long long workers = min((long long)max_workers, total);
     const long long f0 = first * p.Hkv + (long long)h * t.nrec;
     w0 = worker_of(f0, total, workers);
     w1 = worker_of(f0 + t.nrec - 1, total, workers);
-    if (w0 == w1) return;  // one worker had all of it
+    mine = w0 != w1;  // else one worker had all of it
   }
-  const int rho = t.rho0 + n;
-  const long long qrow = (long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (!mine && WPR == 1) return;
+  if (WPR == W && !mine) return;  // the whole block
   float acc[V], sum = 0.f, mx = -INFINITY;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (long long w = w0 + warp; w <= w1; w += 4 * W) {
+  for (long long w = w0 + sub; mine && w <= w1; w += 4 * WPR) {
     float ls[4], v[4][V];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const long long wk = w + k * W;
+      const long long wk = w + k * WPR;
       const bool live = wk <= w1;
       // the first worker's part is its last (slot 1), the others' their first (slot 0)
       const long long r = (wk * 2 + (wk == w0 ? 1 : 0)) * p.RV + n;
@@ -854,24 +856,36 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int
       for (int i = 0; i < V; ++i) acc[i] += g * v[k][i];
     }
   }
+  if (WPR > 1) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = acc[i];
-  if (lane == 0) s_m[warp] = mx, s_l[warp] = sum;
-  __syncthreads();
-  if (tid < HD) {
-    float m = -INFINITY;
+    for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = acc[i];
+    if (lane == 0) s_m[warp] = mx, s_l[warp] = sum;
+    __syncthreads();
+    if (!mine || sub != 0) return;
+    mx = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < W; ++i) m = fmaxf(m, s_m[i]);
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f, o = 0.f;
+    for (int i = 0; i < WPR; ++i) mx = fmaxf(mx, s_m[warp + i]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < W; ++i) {
-      const float g = ex2_approx(s_m[i] - ref);
-      l += s_l[i] * g, o += s_o[i][tid] * g;
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) {
+      const float g = ex2_approx(s_m[warp + i] - ref);
+      sum += s_l[warp + i] * g;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] += s_o[warp + i][lane * V + k] * g;
     }
-    p.o[qrow * HD + tid] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
-    if (tid == 0 && p.lse) p.lse[qrow] = l == 0.f ? -INFINITY : (ref + log2f(l)) * 0.6931471805599453f;
   }
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  const int rho = t.rho0 + n;
+  const long long qrow = (long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G;
+  const float f = sum == 0.f ? 0.f : 1.f / sum;
+  __nv_bfloat16* out = p.o + qrow * HD + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<__nv_bfloat162*>(out + i) = __floats2bfloat162_rn(acc[i] * f, acc[i + 1] * f);
+  if (lane == 0 && p.lse) p.lse[qrow] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------ host
@@ -927,9 +941,19 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& pl, double bytes
     Prof prof(PK_ATTN_FWD, flops, bytes, st);
     GPTK_CUDA(launch_pdl(kern, dim3(grid), dim3(C::WARPS * 32), C::SMEM, st, a));
   }
+  // warps a row of the join: by the parts that a row has on average when every worker is busy
+  const long long segs = pl.E * a.Hkv, workers = (long long)grid * C::WARPS;
+  const long long parts = workers / segs;
+  const int rows = (int)(segs * pl.RV);
   Prof prof(PK_ATTN_FWD, 0, 0, st);
-  GPTK_CUDA(launch_pdl(kv_join_kernel<G::HD, SPARSE>, dim3((unsigned)(pl.E * a.Hkv * pl.RV)), dim3(kJoinThreads), 0, st,
-                       a, pl.RT, (int)C::U, grid * C::WARPS));
+  auto join = [&](auto kern, int wpr) {
+    const unsigned int per = kJoinThreads / 32 / wpr;
+    return launch_pdl(kern, dim3((rows + per - 1) / per), dim3(kJoinThreads), 0, st, a, pl.RT, (int)C::U, (int)workers,
+                      rows);
+  };
+  GPTK_CUDA(parts >= 24  ? join(kv_join_kernel<G::HD, SPARSE, 8>, 8)
+            : parts >= 6 ? join(kv_join_kernel<G::HD, SPARSE, 2>, 2)
+                         : join(kv_join_kernel<G::HD, SPARSE, 1>, 1));
   return ST_OK;
 }
 
@@ -961,6 +985,14 @@ GPT_API int gpt_op_attention_kv(const gpt_kv_cache* cache, const gpt_kv_batch* b
     return set_error(ST_INVALID_ARG, "attention_kv: sel and n_sel go together");
   if (n_sel > 0 && window >= 0) return set_error(ST_UNSUPPORTED, "attention_kv: listed blocks take no window");
   if (n_sel > (1 << 24)) return set_error(ST_UNSUPPORTED, "attention_kv: n_sel above 2^24");
+  size_t block_bytes = 0;
+  GPTK_TRY(kv_dispatch(cache, [&](auto g) {
+    block_bytes = (size_t)decltype(g)::TILE * cache->n_kv_head;
+    return (int)ST_OK;
+  }));
+  if (block_bytes > 0x7fffffff) return set_error(ST_UNSUPPORTED, "attention_kv: a block's tiles above 2 GiB");
+  if ((long long)batch->n_seq * batch->max_blocks > 0x7fffffffLL)
+    return set_error(ST_UNSUPPORTED, "attention_kv: block table above 2^31 entries");
   AttendPlan pl;
   GPTK_TRY(attend_plan("attention_kv", cache, batch, M, H, n_sel > 0, &pl));
   if (pl.E == 0 || batch->n_seq == 0 || M == 0) return ST_OK;
@@ -981,6 +1013,7 @@ GPT_API int gpt_op_attention_kv(const gpt_kv_cache* cache, const gpt_kv_batch* b
   a.rows = kv_rows(batch, M);
   if (!batch->cu_new) a.rows.max_new = 1;
   a.n_blocks = cache->n_blocks;
+  a.block_bytes = (unsigned int)block_bytes;
   a.H = H;
   a.Hkv = cache->n_kv_head;
   a.G = H / cache->n_kv_head;

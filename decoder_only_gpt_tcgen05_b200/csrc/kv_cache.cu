@@ -70,6 +70,216 @@ __device__ __forceinline__ Coded<G> encode8(const float2 (&x)[4], float s, float
   return r;
 }
 
+// What a CTA of the append has in hand for all of its heads.
+struct AppendCta {
+  const __nv_bfloat16* src;  // raw row of the block's first new token, at this lane's octet
+  __nv_bfloat16* q_out;      // q row of that token, at this lane's octet
+  uint8_t* tiles;            // of the cache block
+  __nv_bfloat16* bounds;     // of the cache block, or null
+  const float4 *cos, *sin;   // of the first new token, at this lane's first piece
+  long long ld;              // raw row pitch
+  int H, Hkv, nt, slot0, sg, l;
+  bool rope, norm, join;     // join: the block holds tokens of earlier calls
+  float eps;
+};
+
+enum { kRowQ, kRowK, kRowV, kRowMixed };
+
+// The tokens of one head (KIND q, k or v: the warp's lane groups take tokens), or of a head for each
+// lane group (kRowMixed).  u, w hold the first item's octets on entry and, from `next`, the following
+// head's on return: they are loaded one turn ahead, since a turn's arithmetic is about as long as the
+// memory latency.
+template <class G, int KIND>
+__device__ __forceinline__ void append_head(const AppendCta& a_, int h, bool in_range, uint4& u, uint4& w,
+                                            const __nv_bfloat16* next, bool next_live) {
+  constexpr int HD = G::HD, HALF = HD / 2, LPR = HD / 16, SG = 32 / LPR;
+  constexpr bool MIXED = KIND == kRowMixed;
+  constexpr int NW = G::BITS / 4;  // code words of an octet
+  const int H = a_.H, Hkv = a_.Hkv, nt = a_.nt, l = a_.l;
+  const bool is_k = MIXED ? h >= H && h < H + Hkv : KIND == kRowK;
+  const bool is_v = MIXED ? h >= H + Hkv : KIND == kRowV;
+  const bool is_q = !is_k && !is_v;
+  const int tstep = MIXED ? 1 : SG;
+  const __nv_bfloat16* src = a_.src + (long long)h * HD;
+  uint8_t* tile = a_.tiles + (long long)(is_v ? h - H - Hkv : is_k ? h - H : 0) * G::TILE;
+  // a code word's place is a token's offset plus a lane's (key_word and value_octet are sums of both)
+  int off_a, off_c;
+  if (is_v) off_a = G::value_octet(0, l), off_c = G::value_octet(0, LPR + l);
+  else off_a = G::key_word(0, l * NW), off_c = G::key_word(0, (LPR + l) * NW);
+  float mn[16], mx[16];
+  if (KIND == kRowK || MIXED) {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) mn[x] = INFINITY, mx[x] = -INFINITY;
+  }
+  for (int t = MIXED ? 0 : a_.sg, tb = 0; tb < nt; tb += tstep, t += tstep) {
+    const bool live = in_range && t < nt;
+    float2 a[4], c[4];
+    {
+      const unsigned int uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        a[x] = make_float2(bf16_lo(uu[x]), bf16_hi(uu[x]));
+        c[x] = make_float2(bf16_lo(ww[x]), bf16_hi(ww[x]));
+      }
+    }
+    {
+      const bool more = tb + tstep < nt, take = more ? in_range && t + tstep < nt : next_live;
+      const uint4* p = reinterpret_cast<const uint4*>(more ? src + (t + tstep) * a_.ld : next);
+      u = take ? __ldg(p) : make_uint4(0, 0, 0, 0);
+      w = take ? __ldg(p + LPR) : make_uint4(0, 0, 0, 0);
+    }
+    // The norm's factor r = rsqrt(mean x^2 + eps) scales a whole row, so RoPE and the largest value
+    // are taken on the raw row (max |r x| = r max |x|) and the reductions of both run together.
+    float ss = 0.f, ma = 0.f, mc = 0.f;  // sum of squares; max |x| of each group, a NaN stays
+    if (KIND != kRowV && a_.norm) {
+      float2 s2 = fmul2(a[0], a[0]);
+#pragma unroll
+      for (int x = 1; x < 4; ++x) s2 = ffma2(a[x], a[x], s2);
+#pragma unroll
+      for (int x = 0; x < 4; ++x) s2 = ffma2(c[x], c[x], s2);
+      ss = s2.x + s2.y;
+    }
+    if (KIND != kRowV && a_.rope && live && !is_v) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const float4 co = a_.cos[t * (HALF / 4) + y * LPR], si = a_.sin[t * (HALF / 4) + y * LPR];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float2 co2 = x ? make_float2(co.z, co.w) : make_float2(co.x, co.y);
+          const float2 si2 = x ? make_float2(si.z, si.w) : make_float2(si.x, si.y);
+          const float2 x1 = a[2 * y + x], x2 = c[2 * y + x];
+          a[2 * y + x] = ffma2(x1, co2, fmul2(x2, make_float2(-si2.x, -si2.y)));
+          c[2 * y + x] = ffma2(x1, si2, fmul2(x2, co2));
+        }
+      }
+    }
+    if (KIND != kRowQ) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        ma = max_nan(max_nan(ma, fabsf(a[x].x)), fabsf(a[x].y));
+        mc = max_nan(max_nan(mc, fabsf(c[x].x)), fabsf(c[x].y));
+      }
+      if (G::NG == 1) ma = max_nan(ma, mc);
+    }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) {
+      if (KIND != kRowV) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (KIND != kRowQ) ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, o));
+      if (KIND != kRowQ && G::NG == 2) mc = max_nan(mc, __shfl_xor_sync(0xffffffffu, mc, o));
+    }
+    if (KIND != kRowV && a_.norm) {
+      const float r = is_v ? 1.f : rsqrtf(ss / HD + a_.eps);
+      const float2 r2 = make_float2(r, r);
+      ma *= r, mc *= r;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) a[x] = fmul2(a[x], r2), c[x] = fmul2(c[x], r2);
+    }
+    if (G::NG == 1) mc = ma;
+    if ((KIND == kRowQ || MIXED) && live && is_q) {
+      uint4 ou, ow;
+      unsigned int* uu = &ou.x;
+      unsigned int* ww = &ow.x;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const __nv_bfloat162 pu = __floats2bfloat162_rn(a[x].x, a[x].y);
+        const __nv_bfloat162 pw = __floats2bfloat162_rn(c[x].x, c[x].y);
+        uu[x] = *reinterpret_cast<const unsigned int*>(&pu);
+        ww[x] = *reinterpret_cast<const unsigned int*>(&pw);
+      }
+      uint4* p = reinterpret_cast<uint4*>(a_.q_out + ((long long)t * H + h) * HD);
+      p[0] = ou;
+      p[LPR] = ow;
+    }
+    if (KIND != kRowQ && live && !is_q) {
+      // scale = bf16(max / TOP), and the codes are taken against the rounded scale, so its
+      // rounding costs no more than the codes' own half step.  A group that holds an infinity or
+      // a NaN has a NaN scale; one whose scale would be below the normal range reads as zeros.
+      float sf[2], inv[2];
+#pragma unroll
+      for (int g = 0; g < G::NG; ++g) {
+        const float m = g ? mc : ma;
+        constexpr float RT = 1.f / G::TOP;
+        const float q = m * RT;  // and its residual: m / TOP correctly rounded
+        float v = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q, (float)G::TOP, m), RT, q)));
+        if (v < FLT_MIN) v = 0.f;
+        if (!(m < INFINITY)) v = __uint_as_float(0x7fc00000u);
+        sf[g] = v;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[g]) : "f"(v));
+        if (v == 0.f) inv[g] = 0.f;
+      }
+      if (G::NG == 1) sf[1] = sf[0], inv[1] = inv[0];
+      const Coded<G> ca = encode8<G>(a, sf[0], inv[0]), cc = encode8<G>(c, sf[1], inv[1]);
+      if ((KIND == kRowK || MIXED) && is_k && a_.bounds != nullptr) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const float2 va = fmul2(ca.n[x], make_float2(sf[0], sf[0])), vc = fmul2(cc.n[x], make_float2(sf[1], sf[1]));
+          mn[2 * x] = min_nan(mn[2 * x], va.x), mx[2 * x] = max_nan(mx[2 * x], va.x);
+          mn[2 * x + 1] = min_nan(mn[2 * x + 1], va.y), mx[2 * x + 1] = max_nan(mx[2 * x + 1], va.y);
+          mn[8 + 2 * x] = min_nan(mn[8 + 2 * x], vc.x), mx[8 + 2 * x] = max_nan(mx[8 + 2 * x], vc.x);
+          mn[9 + 2 * x] = min_nan(mn[9 + 2 * x], vc.y), mx[9 + 2 * x] = max_nan(mx[9 + 2 * x], vc.y);
+        }
+      }
+      const int slot = a_.slot0 + t, i = slot % kKvRec;
+      uint8_t* rec = tile + slot / kKvRec * G::REC;
+      uint8_t* at = rec + (is_v ? G::value_octet(i, 0) - G::VCODES : G::key_word(i, 0));
+      if (is_v && NW == 2) {
+        *reinterpret_cast<uint2*>(at + off_a) = make_uint2(ca.w[0], ca.w[NW - 1]);
+        *reinterpret_cast<uint2*>(at + off_c) = make_uint2(cc.w[0], cc.w[NW - 1]);
+      } else {  // the two words of an 8-bit key octet belong to neighbouring lanes' pieces
+        *reinterpret_cast<unsigned int*>(at + off_a) = ca.w[0];
+        *reinterpret_cast<unsigned int*>(at + off_c) = cc.w[0];
+        if (NW == 2) {
+          *reinterpret_cast<unsigned int*>(at + off_a + G::KP) = ca.w[NW - 1];
+          *reinterpret_cast<unsigned int*>(at + off_c + G::KP) = cc.w[NW - 1];
+        }
+      }
+      if (l < G::NG) {
+        __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(rec + (is_v ? G::VSCALE : G::KSCALE));
+        sp[i * G::NG + l] = __float2bfloat16_rn(l == 0 ? sf[0] : sf[1]);
+      }
+    }
+  }
+  if ((KIND == kRowK || MIXED) && a_.bounds != nullptr && (!MIXED || __any_sync(0xffffffffu, is_k))) {
+    if (!MIXED) {
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          mn[x] = min_nan(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], o));
+          mx[x] = max_nan(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
+        }
+      }
+    }
+    if (is_k && in_range && (MIXED || a_.sg == 0)) {
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        __nv_bfloat16* bp = a_.bounds + ((h - H) * 2LL + q) * HD;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          uint4* p = reinterpret_cast<uint4*>(bp) + l + hf * LPR;
+          uint4 bu = a_.join ? *p : make_uint4(0, 0, 0, 0);
+          unsigned int* uu = &bu.x;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            float v[2];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float old = y ? bf16_hi(uu[x]) : bf16_lo(uu[x]);
+              const float f = (q ? mx : mn)[8 * hf + 2 * x + y];
+              v[y] = !a_.join ? f : q ? max_nan(old, f) : min_nan(old, f);
+            }
+            // rounded outward, so that they stay bounds
+            const __nv_bfloat16 e0 = q ? __float2bfloat16_ru(v[0]) : __float2bfloat16_rd(v[0]);
+            const __nv_bfloat16 e1 = q ? __float2bfloat16_ru(v[1]) : __float2bfloat16_rd(v[1]);
+            uu[x] = (unsigned int)__bfloat16_as_ushort(e0) | ((unsigned int)__bfloat16_as_ushort(e1) << 16);
+          }
+          *p = bu;
+        }
+      }
+    }
+  }
+}
+
 template <class G>
 __global__ void __launch_bounds__(kAppendThreads)
 kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_per_seq, uint8_t* __restrict__ tiles,
@@ -100,25 +310,29 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
     return;
   }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sg = lane / LPR, l = lane % LPR;
-  const bool wide = nt >= SG;       // the groups take tokens of one head; else a head each
+  const bool wide = nt >= SG;       // the lane groups take tokens of one head; else a head each
   const int heads = H + 2 * Hkv;
   const int hstep = wide ? 1 : SG;  // heads of a warp at a time
-  const int tstep = wide ? SG : 1;  // tokens of a warp at a time
-  const long long ld = (long long)heads * HD;
-  const int warps = gridDim.y * (kAppendThreads / 32);
-  const __nv_bfloat16* src = qkv + (s.row0 + (t0 - pos0)) * ld + 8 * l;
-  // a (head, token) item's two octets; loaded one turn ahead, since a turn's arithmetic is about as
-  // long as the memory latency
-  auto load = [&](int h0, int tb, uint4& u, uint4& w) {
-    const int h = wide ? h0 : h0 + sg, t = wide ? tb + sg : tb;
-    const bool live = h < heads && t < nt;
-    const uint4* p = reinterpret_cast<const uint4*>(src + t * ld + (long long)h * HD);
-    u = live ? __ldg(p) : make_uint4(0, 0, 0, 0);
-    w = live ? __ldg(p + LPR) : make_uint4(0, 0, 0, 0);
-  };
+  const long long row = s.row0 + (t0 - pos0);
+  AppendCta c;
+  c.ld = (long long)heads * HD;
+  c.src = qkv + row * c.ld + 8 * l;
+  c.q_out = q_out + row * H * HD + 8 * l;
+  c.tiles = tiles + (long long)phys * Hkv * G::TILE;
+  c.bounds = bounds ? bounds + (long long)phys * Hkv * 2 * HD : nullptr;
+  c.cos = &s_cos[0][l], c.sin = &s_sin[0][l];
+  c.H = H, c.Hkv = Hkv, c.nt = nt, c.slot0 = t0 - blk * kKvBlock, c.sg = sg, c.l = l;
+  c.rope = rope, c.norm = qk_norm, c.join = c.slot0 > 0, c.eps = eps;
+  const int hs = gridDim.y * (kAppendThreads / 32) * hstep;
   int h0 = (blockIdx.y * (kAppendThreads / 32) + warp) * hstep;
-  uint4 u, w;
-  load(h0, 0, u, w);
+  // the first item of head step h0 for this lane
+  auto first = [&](int h0) { return c.src + (wide ? sg * c.ld + (long long)h0 * HD : (long long)(h0 + sg) * HD); };
+  auto first_live = [&](int h0) { return wide ? h0 < heads && sg < nt : h0 + sg < heads; };
+  uint4 u = make_uint4(0, 0, 0, 0), w = u;
+  if (first_live(h0)) {
+    u = __ldg(reinterpret_cast<const uint4*>(first(h0)));
+    w = __ldg(reinterpret_cast<const uint4*>(first(h0)) + LPR);
+  }
   if (rope) {
     float* fc = reinterpret_cast<float*>(s_cos);
     float* fs = reinterpret_cast<float*>(s_sin);
@@ -131,188 +345,13 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
     }
     __syncthreads();
   }
-  for (; h0 < heads; h0 += warps * hstep) {
-    const int h = wide ? h0 : h0 + sg;
-    const bool is_k = h >= H && h < H + Hkv, is_v = h >= H + Hkv;
-    const bool any_kv = __any_sync(0xffffffffu, h >= H), any_qk = __any_sync(0xffffffffu, !is_v);
-    const int kvh = is_v ? h - H - Hkv : h - H;
-    uint8_t* head_tile = tiles + ((long long)phys * Hkv + kvh) * G::TILE;
-    float mn[16], mx[16];
-#pragma unroll
-    for (int x = 0; x < 16; ++x) mn[x] = INFINITY, mx[x] = -INFINITY;
-    for (int tb = 0; tb < nt; tb += tstep) {
-      const int t = wide ? tb + sg : tb;
-      const bool live = h < heads && t < nt;
-      float2 a[4], c[4];
-      {
-        const unsigned int uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          a[x] = make_float2(bf16_lo(uu[x]), bf16_hi(uu[x]));
-          c[x] = make_float2(bf16_lo(ww[x]), bf16_hi(ww[x]));
-        }
-      }
-      if (tb + tstep < nt) load(h0, tb + tstep, u, w);
-      else load(h0 + warps * hstep, 0, u, w);
-      // The norm's factor r = rsqrt(mean x^2 + eps) scales a whole row, so RoPE and the largest value
-      // are taken on the raw row (max |r x| = r max |x|) and the reductions of both run together.
-      float ss = 0.f;
-      if (qk_norm && any_qk) {
-        float2 s2 = fmul2(a[0], a[0]);
-#pragma unroll
-        for (int x = 1; x < 4; ++x) s2 = ffma2(a[x], a[x], s2);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) s2 = ffma2(c[x], c[x], s2);
-        ss = s2.x + s2.y;
-      }
-      if (rope && live && !is_v) {
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const float4 co = s_cos[t][y * LPR + l], si = s_sin[t][y * LPR + l];
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const float2 co2 = x ? make_float2(co.z, co.w) : make_float2(co.x, co.y);
-            const float2 si2 = x ? make_float2(si.z, si.w) : make_float2(si.x, si.y);
-            const float2 x1 = a[2 * y + x], x2 = c[2 * y + x];
-            a[2 * y + x] = ffma2(x1, co2, fmul2(x2, make_float2(-si2.x, -si2.y)));
-            c[2 * y + x] = ffma2(x1, si2, fmul2(x2, co2));
-          }
-        }
-      }
-      float ma = 0.f, mc = 0.f;  // max |x| of each group; a NaN stays
-      if (any_kv) {
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          ma = max_nan(max_nan(ma, fabsf(a[x].x)), fabsf(a[x].y));
-          mc = max_nan(max_nan(mc, fabsf(c[x].x)), fabsf(c[x].y));
-        }
-        if (G::NG == 1) ma = max_nan(ma, mc);
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          ma = max_nan(ma, __shfl_xor_sync(0xffffffffu, ma, o));
-          if (G::NG == 2) mc = max_nan(mc, __shfl_xor_sync(0xffffffffu, mc, o));
-        }
-      } else {
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      }
-      if (qk_norm && any_qk) {
-        const float r = is_v ? 1.f : rsqrtf(ss / HD + eps);
-        const float2 r2 = make_float2(r, r);
-        ma *= r, mc *= r;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) a[x] = fmul2(a[x], r2), c[x] = fmul2(c[x], r2);
-      }
-      if (G::NG == 1) mc = ma;
-      if (live && !is_k && !is_v) {
-        uint4 ou, ow;
-        unsigned int* uu = &ou.x;
-        unsigned int* ww = &ow.x;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const __nv_bfloat162 pu = __floats2bfloat162_rn(a[x].x, a[x].y);
-          const __nv_bfloat162 pw = __floats2bfloat162_rn(c[x].x, c[x].y);
-          uu[x] = *reinterpret_cast<const unsigned int*>(&pu);
-          ww[x] = *reinterpret_cast<const unsigned int*>(&pw);
-        }
-        uint4* p = reinterpret_cast<uint4*>(q_out + ((s.row0 + (t0 - pos0) + (long long)t) * H + h) * HD);
-        p[l] = ou;
-        p[LPR + l] = ow;
-      }
-      if (live && (is_k || is_v)) {
-        // scale = bf16(max / TOP), and the codes are taken against the rounded scale, so its
-        // rounding costs no more than the codes' own half step.  A group that holds an infinity or
-        // a NaN has a NaN scale; one whose scale would be below the normal range reads as zeros.
-        float sf[2], inv[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float m = g ? mc : ma;
-          constexpr float RT = 1.f / G::TOP;
-          const float q = m * RT;  // and its residual: m / TOP correctly rounded
-          float v = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q, (float)G::TOP, m), RT, q)));
-          if (v < FLT_MIN) v = 0.f;
-          if (!(m < INFINITY)) v = __uint_as_float(0x7fc00000u);
-          sf[g] = v;
-          asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv[g]) : "f"(v));
-          if (v == 0.f) inv[g] = 0.f;
-          if (G::NG == 1) {
-            sf[1] = sf[0], inv[1] = inv[0];
-            break;
-          }
-        }
-        const Coded<G> ca = encode8<G>(a, sf[0], inv[0]), cc = encode8<G>(c, sf[1], inv[1]);
-        if (is_k && bounds != nullptr) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float2 va = fmul2(ca.n[x], make_float2(sf[0], sf[0])), vc = fmul2(cc.n[x], make_float2(sf[1], sf[1]));
-            mn[2 * x] = min_nan(mn[2 * x], va.x), mx[2 * x] = max_nan(mx[2 * x], va.x);
-            mn[2 * x + 1] = min_nan(mn[2 * x + 1], va.y), mx[2 * x + 1] = max_nan(mx[2 * x + 1], va.y);
-            mn[8 + 2 * x] = min_nan(mn[8 + 2 * x], vc.x), mx[8 + 2 * x] = max_nan(mx[8 + 2 * x], vc.x);
-            mn[9 + 2 * x] = min_nan(mn[9 + 2 * x], vc.y), mx[9 + 2 * x] = max_nan(mx[9 + 2 * x], vc.y);
-          }
-        }
-        const int slot = t0 + t - blk * kKvBlock, i = slot % kKvRec;
-        uint8_t* rec = head_tile + slot / kKvRec * G::REC;
-        if (is_k) {
-#pragma unroll
-          for (int x = 0; x < G::BITS / 4; ++x) {
-            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, l * (G::BITS / 4) + x)) = ca.w[x];
-            *reinterpret_cast<unsigned int*>(rec + G::key_word(i, (LPR + l) * (G::BITS / 4) + x)) = cc.w[x];
-          }
-        } else if (G::BITS == 4) {
-          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, l)) = ca.w[0];
-          *reinterpret_cast<unsigned int*>(rec + G::value_octet(i, LPR + l)) = cc.w[0];
-        } else {
-          *reinterpret_cast<uint2*>(rec + G::value_octet(i, l)) = make_uint2(ca.w[0], ca.w[G::BITS / 4 - 1]);
-          *reinterpret_cast<uint2*>(rec + G::value_octet(i, LPR + l)) = make_uint2(cc.w[0], cc.w[G::BITS / 4 - 1]);
-        }
-        if (l < G::NG) {
-          __nv_bfloat16* sp = reinterpret_cast<__nv_bfloat16*>(rec + (is_k ? G::KSCALE : G::VSCALE));
-          sp[i * G::NG + l] = __float2bfloat16_rn(l == 0 ? sf[0] : sf[1]);
-        }
-      }
-    }
-    if (bounds != nullptr && __any_sync(0xffffffffu, is_k)) {
-      if (wide) {
-#pragma unroll
-        for (int o = LPR; o < 32; o <<= 1) {
-#pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            mn[x] = min_nan(mn[x], __shfl_xor_sync(0xffffffffu, mn[x], o));
-            mx[x] = max_nan(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], o));
-          }
-        }
-      }
-      if (is_k && (!wide || sg == 0)) {
-        const bool join = t0 > blk * kKvBlock;  // tokens of earlier calls are in the block
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          __nv_bfloat16* bp = bounds + (((long long)phys * Hkv + kvh) * 2 + q) * HD;
-#pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            uint4* p = reinterpret_cast<uint4*>(bp) + l + hf * LPR;
-            uint4 bu = join ? *p : make_uint4(0, 0, 0, 0);
-            unsigned int* uu = &bu.x;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float v[2];
-#pragma unroll
-              for (int y = 0; y < 2; ++y) {
-                const float old = y ? bf16_hi(uu[x]) : bf16_lo(uu[x]);
-                const float f = (q ? mx : mn)[8 * hf + 2 * x + y];
-                v[y] = !join ? f : q ? max_nan(old, f) : min_nan(old, f);
-              }
-              // rounded outward, so that they stay bounds
-              const __nv_bfloat16 e0 = q ? __float2bfloat16_ru(v[0]) : __float2bfloat16_rd(v[0]);
-              const __nv_bfloat16 e1 = q ? __float2bfloat16_ru(v[1]) : __float2bfloat16_rd(v[1]);
-              uu[x] = (unsigned int)__bfloat16_as_ushort(e0) | ((unsigned int)__bfloat16_as_ushort(e1) << 16);
-            }
-            *p = bu;
-          }
-        }
-      }
-    }
+  for (; h0 < heads; h0 += hs) {
+    const __nv_bfloat16* next = first(h0 + hs);
+    const bool nl = first_live(h0 + hs);
+    if (!wide) append_head<G, kRowMixed>(c, h0 + sg, h0 + sg < heads, u, w, next, nl);
+    else if (h0 < H) append_head<G, kRowQ>(c, h0, true, u, w, next, nl);
+    else if (h0 < H + Hkv) append_head<G, kRowK>(c, h0, true, u, w, next, nl);
+    else append_head<G, kRowV>(c, h0, true, u, w, next, nl);
   }
 }
 

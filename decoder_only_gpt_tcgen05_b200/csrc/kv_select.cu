@@ -15,7 +15,7 @@
 namespace gptk {
 
 constexpr int kScoreThreads = 256;
-constexpr int kScoreChunk = 128;  // blocks a CTA scores
+constexpr int kScoreChunk = 64;  // blocks a CTA scores: two turns, whose loads are issued together
 
 // One CTA: one token, one kv head, kScoreChunk blocks.  Eight lanes take a block, 16-byte pieces of
 // both bounds each.  Reads 4 HD bytes a block.  ONE: one query head a kv head.  Loops stay rolled
@@ -59,22 +59,28 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
   }
   __syncthreads();
   const int l = threadIdx.x & 7;
-#pragma unroll 1
-  for (int jb = j0; jb < j1; jb += kScoreThreads / 8) {
-    const int j = jb + (threadIdx.x >> 3);
-    const bool here = j < j1, live = here && j < nb;
-    const int phys = here ? s_phys[j - j0] : 0;
-    const uint4* p = reinterpret_cast<const uint4*>(bounds + ((long long)max(phys, 0) * Hkv + h) * 2 * HD);
-    double acc = 0.0;
-    uint4 lo[NC], hi[NC];
+  constexpr int TURN = kScoreThreads / 8, TURNS = kScoreChunk / TURN;
+  uint4 lo[TURNS][NC], hi[TURNS][NC];
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    const int j = j0 + i * TURN + (threadIdx.x >> 3);
+    const bool live = j < min(j1, nb);
+    const int phys = live ? max(s_phys[j - j0], 0) : 0;
+    const uint4* p = reinterpret_cast<const uint4*>(bounds + ((long long)phys * Hkv + h) * 2 * HD);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      lo[c] = live ? __ldg(p + c * 8 + l) : make_uint4(0, 0, 0, 0);
-      hi[c] = live ? __ldg(p + HD / 8 + c * 8 + l) : make_uint4(0, 0, 0, 0);
+      lo[i][c] = live ? __ldg(p + c * 8 + l) : make_uint4(0, 0, 0, 0);
+      hi[i][c] = live ? __ldg(p + HD / 8 + c * 8 + l) : make_uint4(0, 0, 0, 0);
     }
+  }
+#pragma unroll
+  for (int i = 0; i < TURNS; ++i) {
+    const int j = j0 + i * TURN + (threadIdx.x >> 3);
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};  // four chains: the fp64 add's latency is many cycles
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      const unsigned int ul[4] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w}, uh[4] = {hi[c].x, hi[c].y, hi[c].z, hi[c].w};
+      const uint4 vl = lo[i][c], vh = hi[i][c];
+      const unsigned int ul[4] = {vl.x, vl.y, vl.z, vl.w}, uh[4] = {vh.x, vh.y, vh.z, vh.w};
       const double* qp = s_q + c * 64 + l;
       float a[8], e[8];
 #pragma unroll
@@ -86,7 +92,7 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           const double qv = qp[x * 8];
-          acc = fma(qv, (double)(qv > 0.0 ? e[x] : a[x]), acc);
+          acc[x % 4] = fma(qv, (double)(qv > 0.0 ? e[x] : a[x]), acc[x % 4]);
         }
       } else {
         double da[8], de[8];
@@ -97,14 +103,15 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const double qv = qp[g * HD + x * 8];
-            acc = fma(qv, qv > 0.0 ? de[x] : da[x], acc);
+            acc[x % 4] = fma(qv, qv > 0.0 ? de[x] : da[x], acc[x % 4]);
           }
         }
       }
     }
+    double sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (here && l == 0) out[j] = !live ? -INFINITY : phys < 0 ? __uint_as_float(0x7fc00000u) : (float)acc;
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (j < j1 && l == 0) out[j] = j >= nb ? -INFINITY : s_phys[j - j0] < 0 ? __uint_as_float(0x7fc00000u) : (float)sum;
   }
 }
 
@@ -223,7 +230,7 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     return set_error(ST_INVALID_ARG, "kv_select: n_select >= 1 and n_first + n_last <= n_select are needed");
   if ((long long)M * Hkv > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_select: M x n_kv_head too large");
   const long long chunks = ((long long)batch->max_blocks + kScoreChunk - 1) / kScoreChunk;
-  if (chunks > 65535) return set_error(ST_UNSUPPORTED, "kv_select: max_blocks above 128 x 65535");
+  if (chunks > 65535) return set_error(ST_UNSUPPORTED, "kv_select: max_blocks above 64 x 65535");
   if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
   if (!q || !blocks || !scores) return set_error(ST_INVALID_ARG, "kv_select: null q, blocks or scores");
   if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(blocks) & 3) ||

@@ -47,7 +47,7 @@ def _check(t: torch.Tensor, name: str, dtype, dev, shape=None) -> None:
 def _out(t, name: str, shape, dtype, dev) -> torch.Tensor:
     """The caller's output tensor, checked, or a new one."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(*shape, dtype=dtype, device=dev)  # (sizes one by one: parsed faster than a tuple)
     _check(t, name, dtype, dev, shape)
     return t
 
@@ -110,7 +110,7 @@ class KVCache:
         _check(qkv, "qkv", torch.bfloat16, self.device, (M, (n_head + 2 * self.n_kv_head) * self.head_dim))
         assert batch.device == self.device, "batch: on another device than the cache"
         if q is None:
-            q = torch.empty((M, n_head * self.head_dim), dtype=torch.bfloat16, device=self.device)
+            q = torch.empty(M, n_head * self.head_dim, dtype=torch.bfloat16, device=self.device)
         else:
             _check(q, "q", torch.bfloat16, self.device, (M, n_head * self.head_dim))
         _launch("gpt_op_kv_append", self.device, self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope),
@@ -168,10 +168,10 @@ class KVCache:
             n_sel = blocks.shape[-1]
             _check(blocks, "blocks", torch.int32, self.device, (M, self.n_kv_head, n_sel))
             assert n_sel > 0, "blocks: at least one entry a list"
-        o = _out(o, "o", (M, H * self.head_dim), torch.bfloat16, self.device)
+        o = torch.empty_like(q) if o is None else _out(o, "o", q.shape, torch.bfloat16, self.device)
         lse = _out(lse, "lse", (M, H), torch.float32, self.device)
         if scratch is None:
-            scratch = torch.empty(self.scratch_bytes(batch, M, H, n_sel), dtype=torch.uint8, device=self.device)
+            scratch = self.tiles.new_empty(self.scratch_bytes(batch, M, H, n_sel))
         else:
             _check(scratch, "scratch", torch.uint8, self.device)
         _launch("gpt_op_attention_kv", self.device, self._ref, batch._ref, q.data_ptr(), M, H, int(window),
