@@ -70,6 +70,44 @@ __device__ __forceinline__ Coded<G> encode8(const float2 (&x)[4], float s, float
   return r;
 }
 
+// cos and sin of an angle of any size: reduced in fp64 to r in [-pi/4, pi/4] and a quarter turn k (adding
+// 1.5 2^52 rounds to the integer, whose low bits it leaves in the sum's low word), then the Taylor sums to
+// r^9 and r^10 in fp32, whose remainders (1.8e-9 and 1.2e-10 at pi/4) are below fp32's rounding.  The
+// arguments reach pi/4 only, so this takes a third of the instructions of the general functions.
+__device__ __forceinline__ void rope_angle(double a, float* c, float* s) {
+  constexpr double kShift = 6755399441055744.0;  // 1.5 2^52
+  const double t = fma(a, 0.6366197723675814, kShift);
+  const int k = __double2loint(t);
+  const float r = (float)fma(kShift - t, 1.5707963267948966, a), z = r * r;
+  float sn = fmaf(z, 1.f / 362880.f, -1.f / 5040.f);
+  sn = fmaf(sn, z, 1.f / 120.f);
+  sn = fmaf(sn, z, -1.f / 6.f);
+  sn = fmaf(sn * z, r, r);
+  float cs = fmaf(z, -1.f / 3628800.f, 1.f / 40320.f);
+  cs = fmaf(cs, z, -1.f / 720.f);
+  cs = fmaf(cs, z, 1.f / 24.f);
+  cs = fmaf(cs, z, -0.5f);
+  cs = fmaf(cs, z, 1.f);
+  const bool odd = k & 1;
+  const float x = odd ? sn : cs, y = odd ? cs : sn;
+  *c = (k + 1) & 2 ? -x : x;
+  *s = k & 2 ? -y : y;
+}
+
+// The raw rows come through a ring of asynchronous copies, private to each lane: it reads back the 32
+// bytes a turn that it copied itself, so the ring needs no barrier.  Three turns in flight by 16 warps
+// are 48 KB an SM, what HBM's latency asks for; loads into registers one turn ahead were a third of that
+// and bounded the kernel (63 us against 50 for 18.6k tokens of 30 heads).
+constexpr int kAppendRing = 4;
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // What a CTA of the append has in hand for all of its heads.
 struct AppendCta {
   const __nv_bfloat16* src;  // raw row of the block's first new token, at this lane's octet
@@ -81,17 +119,37 @@ struct AppendCta {
   int H, Hkv, nt, slot0, sg, l;
   bool rope, norm, join;     // join: the block holds tokens of earlier calls
   float eps;
+  // the copying iterator: head step, token turn, and the shared address of this lane's ring
+  int f_h, f_tb, heads, hs;
+  bool wide;
+  uint32_t ring;
+  int turn;                  // turns read so far
 };
+
+// Starts the copy of the next turn's item (head f_h, or f_h + sg; token f_tb + sg, or f_tb) into the slot
+// of turn `turn`, if there is one; a group either way, so that the waits can count.
+template <class G>
+__device__ __forceinline__ void append_copy(AppendCta& c, int turn) {
+  constexpr int LPR = G::HD / 16, SG = 32 / LPR;
+  if (c.f_h < c.heads) {
+    const int h = c.wide ? c.f_h : c.f_h + c.sg, t = c.wide ? c.f_tb + c.sg : c.f_tb;
+    const bool live = h < c.heads && t < c.nt;
+    const __nv_bfloat16* p = c.src + (live ? t * c.ld + (long long)h * G::HD : 0);
+    const uint32_t dst = c.ring + turn % kAppendRing * 1024;
+    copy16(dst, p, live);
+    copy16(dst + 512, p + 8 * LPR, live);
+    c.f_tb += c.wide ? SG : 1;
+    if (c.f_tb >= c.nt) c.f_tb = 0, c.f_h += c.hs;
+  }
+  copy_commit();
+}
 
 enum { kRowQ, kRowK, kRowV, kRowMixed };
 
 // The tokens of one head (KIND q, k or v: the warp's lane groups take tokens), or of a head for each
-// lane group (kRowMixed).  u, w hold the first item's octets on entry and, from `next`, the following
-// head's on return: they are loaded one turn ahead, since a turn's arithmetic is about as long as the
-// memory latency.
+// lane group (kRowMixed).
 template <class G, int KIND>
-__device__ __forceinline__ void append_head(const AppendCta& a_, int h, bool in_range, uint4& u, uint4& w,
-                                            const __nv_bfloat16* next, bool next_live) {
+__device__ __forceinline__ void append_head(AppendCta& a_, int h, bool in_range) {
   constexpr int HD = G::HD, HALF = HD / 2, LPR = HD / 16, SG = 32 / LPR;
   constexpr bool MIXED = KIND == kRowMixed;
   constexpr int NW = G::BITS / 4;  // code words of an octet
@@ -100,7 +158,6 @@ __device__ __forceinline__ void append_head(const AppendCta& a_, int h, bool in_
   const bool is_v = MIXED ? h >= H + Hkv : KIND == kRowV;
   const bool is_q = !is_k && !is_v;
   const int tstep = MIXED ? 1 : SG;
-  const __nv_bfloat16* src = a_.src + (long long)h * HD;
   uint8_t* tile = a_.tiles + (long long)(is_v ? h - H - Hkv : is_k ? h - H : 0) * G::TILE;
   // a code word's place is a token's offset plus a lane's (key_word and value_octet are sums of both)
   int off_a, off_c;
@@ -115,18 +172,24 @@ __device__ __forceinline__ void append_head(const AppendCta& a_, int h, bool in_
     const bool live = in_range && t < nt;
     float2 a[4], c[4];
     {
-      const unsigned int uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
+      copy_wait<kAppendRing - 2>();
+      unsigned int uu[4], ww[4];
+      const uint32_t at = a_.ring + a_.turn % kAppendRing * 1024;
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(uu[0]), "=r"(uu[1]), "=r"(uu[2]), "=r"(uu[3])
+                   : "r"(at)
+                   : "memory");
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(ww[0]), "=r"(ww[1]), "=r"(ww[2]), "=r"(ww[3])
+                   : "r"(at + 512)
+                   : "memory");
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         a[x] = make_float2(bf16_lo(uu[x]), bf16_hi(uu[x]));
         c[x] = make_float2(bf16_lo(ww[x]), bf16_hi(ww[x]));
       }
-    }
-    {
-      const bool more = tb + tstep < nt, take = more ? in_range && t + tstep < nt : next_live;
-      const uint4* p = reinterpret_cast<const uint4*>(more ? src + (t + tstep) * a_.ld : next);
-      u = take ? __ldg(p) : make_uint4(0, 0, 0, 0);
-      w = take ? __ldg(p + LPR) : make_uint4(0, 0, 0, 0);
+      append_copy<G>(a_, a_.turn + kAppendRing - 1);  // the slot of the turn before, which has been read
+      ++a_.turn;
     }
     // The norm's factor r = rsqrt(mean x^2 + eps) scales a whole row, so RoPE and the largest value
     // are taken on the raw row (max |r x| = r max |x|) and the reductions of both run together.
@@ -290,7 +353,10 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
   constexpr int SG = 32 / LPR;   // rows of a warp
   // cosines and sines of a token's frequencies, in pieces of four: piece y of lane l (frequencies
   // 8 l + 4 y ..) at y LPR + l, so that a read takes consecutive pieces
-  __shared__ float4 s_cos[kKvBlock][HALF / 4], s_sin[kKvBlock][HALF / 4];
+  extern __shared__ __align__(128) uint8_t append_smem[];
+  float4(*s_cos)[HALF / 4] = reinterpret_cast<float4(*)[HALF / 4]>(append_smem);
+  float4(*s_sin)[HALF / 4] = s_cos + kKvBlock;
+  uint8_t* s_ring = append_smem + 2 * kKvBlock * HALF * 4;
   pdl_wait();
   pdl_trigger();
   const int b = blockIdx.x / blocks_per_seq;
@@ -325,34 +391,27 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
   c.rope = rope, c.norm = qk_norm, c.join = c.slot0 > 0, c.eps = eps;
   const int hs = gridDim.y * (kAppendThreads / 32) * hstep;
   int h0 = (blockIdx.y * (kAppendThreads / 32) + warp) * hstep;
-  // the first item of head step h0 for this lane
-  auto first = [&](int h0) { return c.src + (wide ? sg * c.ld + (long long)h0 * HD : (long long)(h0 + sg) * HD); };
-  auto first_live = [&](int h0) { return wide ? h0 < heads && sg < nt : h0 + sg < heads; };
-  uint4 u = make_uint4(0, 0, 0, 0), w = u;
-  if (first_live(h0)) {
-    u = __ldg(reinterpret_cast<const uint4*>(first(h0)));
-    w = __ldg(reinterpret_cast<const uint4*>(first(h0)) + LPR);
-  }
+  c.heads = heads, c.hs = hs, c.wide = wide, c.f_h = h0, c.f_tb = 0, c.turn = 0;
+  c.ring = smem_u32(s_ring) + warp * kAppendRing * 1024 + lane * 16;
+#pragma unroll
+  for (int i = 0; i < kAppendRing - 1; ++i) append_copy<G>(c, i);
   if (rope) {
     float* fc = reinterpret_cast<float*>(s_cos);
     float* fs = reinterpret_cast<float*>(s_sin);
     for (int x = threadIdx.x; x < nt * HALF; x += kAppendThreads) {
       const int t = x / HALF, at = x - t * HALF;
       const int i = at / 4 % LPR * 8 + at / 4 / LPR * 4 + at % 4;
-      const double a = (double)(t0 + t) * freq.f[i];
-      const float red = (float)(a - rint(a * 0.15915494309189535) * 6.283185307179586);
-      sincosf(red, fs + x, fc + x);
+      rope_angle((double)(t0 + t) * freq.f[i], fc + x, fs + x);
     }
     __syncthreads();
   }
   for (; h0 < heads; h0 += hs) {
-    const __nv_bfloat16* next = first(h0 + hs);
-    const bool nl = first_live(h0 + hs);
-    if (!wide) append_head<G, kRowMixed>(c, h0 + sg, h0 + sg < heads, u, w, next, nl);
-    else if (h0 < H) append_head<G, kRowQ>(c, h0, true, u, w, next, nl);
-    else if (h0 < H + Hkv) append_head<G, kRowK>(c, h0, true, u, w, next, nl);
-    else append_head<G, kRowV>(c, h0, true, u, w, next, nl);
+    if (!wide) append_head<G, kRowMixed>(c, h0 + sg, h0 + sg < heads);
+    else if (h0 < H) append_head<G, kRowQ>(c, h0, true);
+    else if (h0 < H + Hkv) append_head<G, kRowK>(c, h0, true);
+    else append_head<G, kRowV>(c, h0, true);
   }
+  copy_wait<0>();
 }
 
 // ------------------------------------------------------------------ read
@@ -387,41 +446,44 @@ kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tile
   const uint8_t* tile = tiles + ((long long)(bad ? 0 : phys) * Hkv + h) * G::TILE;
   const long long ldo = (long long)Hkv * HD;
   const long long out0 = ((long long)s.row0 - pos0) * ldo + (long long)h * HD;  // of position 0
+  // NT tiles at a time, every load of theirs first
+  constexpr int NT = G::BITS == 4 ? 2 : 1;
 #pragma unroll 1
-  for (int base = t0 & ~15; base < t1; base += 16) {
-    const int slot = base % kKvBlock, i0 = slot % kKvRec;
-    const uint8_t* rec = tile + slot / kKvRec * G::REC;
-    // every load first
-    unsigned int uv[G::VB], uk[2][G::KB / 4];
-    unsigned int sv[4], sk[2];  // scales of this lane's four values and two keys (NG of 16 bits)
+  for (int base0 = t0 & ~15; base0 < t1; base0 += 16 * NT) {
+    unsigned int uv[NT][G::VB], uk[NT][2][G::KB / 4];
+    unsigned int sv[NT][4], sk[NT][2];  // scales of this lane's four values and two keys (NG of 16 bits)
 #pragma unroll
-    for (int p = 0; p < G::VB / 4; ++p) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16));
-      uv[4 * p] = x.x, uv[4 * p + 1] = x.y, uv[4 * p + 2] = x.z, uv[4 * p + 3] = x.w;
-    }
+    for (int n = 0; n < NT; ++n) {
+      const int slot = (base0 + 16 * n) % kKvBlock, i0 = slot % kKvRec;  // (past t1: still in the tile's bytes)
+      const uint8_t* rec = tile + slot / kKvRec * G::REC;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-      for (int p = 0; p < G::KB / G::KP; ++p) {
-        const uint8_t* at = rec + i0 * G::ROWB + p * 64 * G::KP + (r + 8 * hf) * 4 * G::KP + c * G::KP;
-        if (G::KP == 16) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
-          uk[hf][4 * p] = x.x, uk[hf][4 * p + 1] = x.y, uk[hf][4 * p + 2] = x.z, uk[hf][4 * p + 3] = x.w;
-        } else {
-          const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
-          uk[hf][0] = x.x, uk[hf][1] = x.y;
-        }
+      for (int p = 0; p < G::VB / 4; ++p) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16));
+        uv[n][4 * p] = x.x, uv[n][4 * p + 1] = x.y, uv[n][4 * p + 2] = x.z, uv[n][4 * p + 3] = x.w;
       }
-    auto scales = [&](int off, int i) -> unsigned int {
-      const uint8_t* at = rec + off + (i0 + i) * 2 * G::NG;
-      return G::NG == 2 ? __ldg(reinterpret_cast<const unsigned int*>(at))
-                        : __ldg(reinterpret_cast<const unsigned short*>(at));
-    };
 #pragma unroll
-    for (int sl = 0; sl < 4; ++sl) sv[sl] = scales(G::VSCALE, 2 * c + (sl & 1) + 8 * (sl >> 1));
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) sk[hf] = scales(G::KSCALE, r + 8 * hf);
-
+        for (int p = 0; p < G::KB / G::KP; ++p) {
+          const uint8_t* at = rec + i0 * G::ROWB + p * 64 * G::KP + (r + 8 * hf) * 4 * G::KP + c * G::KP;
+          if (G::KP == 16) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+            uk[n][hf][4 * p] = x.x, uk[n][hf][4 * p + 1] = x.y, uk[n][hf][4 * p + 2] = x.z, uk[n][hf][4 * p + 3] = x.w;
+          } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+            uk[n][hf][0] = x.x, uk[n][hf][1] = x.y;
+          }
+        }
+      auto scales = [&](int off, int i) -> unsigned int {
+        const uint8_t* at = rec + off + (i0 + i) * 2 * G::NG;
+        return G::NG == 2 ? __ldg(reinterpret_cast<const unsigned int*>(at))
+                          : __ldg(reinterpret_cast<const unsigned short*>(at));
+      };
+#pragma unroll
+      for (int sl = 0; sl < 4; ++sl) sv[n][sl] = scales(G::VSCALE, 2 * c + (sl & 1) + 8 * (sl >> 1));
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) sk[n][hf] = scales(G::KSCALE, r + 8 * hf);
+    }
     auto scale = [&](unsigned int u, int g) {
       return bad ? __uint_as_float(0x7fc00000u) : G::NG == 2 && g ? bf16_hi(u) : bf16_lo(u);
     };
@@ -438,29 +500,33 @@ kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tile
                           : make_uint4(pair(w[0], 0, sf), pair(w[0], 2, sf), pair(w[1], 0, sf), pair(w[1], 2, sf));
     };
 #pragma unroll
-    for (int sl = 0; sl < 4; ++sl) {
-      const int t = base + 2 * c + (sl & 1) + 8 * (sl >> 1);
-      if (t >= t0 && t < t1) {
-        __nv_bfloat16* out = v_out + out0 + t * ldo + 8 * r;
+    for (int n = 0; n < NT; ++n) {
+      const int base = base0 + 16 * n;
 #pragma unroll
-        for (int wj = 0; wj < HD / 64; ++wj)
-          *reinterpret_cast<uint4*>(out + 64 * wj) =
-              octet(uv + (sl * G::VB + wj * G::BITS) / 4, scale(sv[sl], G::NG == 1 ? 0 : wj));
+      for (int sl = 0; sl < 4; ++sl) {
+        const int t = base + 2 * c + (sl & 1) + 8 * (sl >> 1);
+        if (t >= t0 && t < t1) {
+          __nv_bfloat16* out = v_out + out0 + t * ldo + 8 * r;
+#pragma unroll
+          for (int wj = 0; wj < HD / 64; ++wj)
+            *reinterpret_cast<uint4*>(out + 64 * wj) =
+                octet(uv[n] + (sl * G::VB + wj * G::BITS) / 4, scale(sv[n][sl], G::NG == 1 ? 0 : wj));
+        }
       }
-    }
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int t = base + r + 8 * hf;
-      if (t >= t0 && t < t1) {
-        __nv_bfloat16* out = k_out + out0 + t * ldo;
+      for (int hf = 0; hf < 2; ++hf) {
+        const int t = base + r + 8 * hf;
+        if (t >= t0 && t < t1) {
+          __nv_bfloat16* out = k_out + out0 + t * ldo;
 #pragma unroll
-        for (int wi = 0; wi < G::KB / 4; ++wi) {
-          const float sf = scale(sk[hf], G::NG == 1 ? 0 : wi / 2);
-          if (G::BITS == 4) {
-            *reinterpret_cast<uint4*>(out + 32 * wi + 8 * c) = octet(&uk[hf][wi], sf);
-          } else {
-            *reinterpret_cast<uint2*>(out + 16 * wi + 4 * c) =
-                make_uint2(pair(uk[hf][wi], 0, sf), pair(uk[hf][wi], 2, sf));
+          for (int wi = 0; wi < G::KB / 4; ++wi) {
+            const float sf = scale(sk[n][hf], G::NG == 1 ? 0 : wi / 2);
+            if (G::BITS == 4) {
+              *reinterpret_cast<uint4*>(out + 32 * wi + 8 * c) = octet(&uk[n][hf][wi], sf);
+            } else {
+              *reinterpret_cast<uint2*>(out + 16 * wi + 4 * c) =
+                  make_uint2(pair(uk[n][hf][wi], 0, sf), pair(uk[n][hf][wi], 2, sf));
+            }
           }
         }
       }
@@ -544,7 +610,15 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     if (y > (hw + 7) / 8) y = (hw + 7) / 8;
     KvRows r = kv_rows(batch, M);
     r.max_new = max_new;
-    GPTK_CUDA(launch_pdl(kv_append_kernel<G>, dim3((unsigned)ctas, (unsigned)y), dim3(kAppendThreads), 0, st,
+    constexpr int SMEM = kKvBlock * G::HD * 4 + kAppendThreads / 32 * kAppendRing * 1024;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    GPTK_CUDA(cudaGetDevice(&dev));
+    if (!attr_set[dev & 63]) {
+      GPTK_CUDA(cudaFuncSetAttribute(kv_append_kernel<G>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM));
+      attr_set[dev & 63] = true;
+    }
+    GPTK_CUDA(launch_pdl(kv_append_kernel<G>, dim3((unsigned)ctas, (unsigned)y), dim3(kAppendThreads), SMEM, st,
                          static_cast<const __nv_bfloat16*>(qkv), r, (int)bps, static_cast<uint8_t*>(cache->tiles),
                          static_cast<__nv_bfloat16*>(cache->bounds), (int)cache->n_blocks, H, Hkv, rope, qk_norm, eps, f,
                          static_cast<__nv_bfloat16*>(q_out), device_ctl()));
