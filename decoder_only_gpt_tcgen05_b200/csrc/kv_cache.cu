@@ -358,7 +358,6 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
   float4(*s_sin)[HALF / 4] = s_cos + kKvBlock;
   uint8_t* s_ring = append_smem + 2 * kKvBlock * HALF * 4;
   pdl_wait();
-  pdl_trigger();
   const int b = blockIdx.x / blocks_per_seq;
   const KvSeq s = kv_seq(rows, b);
   if (!s.ok) {
@@ -429,7 +428,6 @@ kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tile
   const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int b = blockIdx.x / blocks_per_seq;
   pdl_wait();
-  pdl_trigger();
   if (h >= Hkv) return;
   const KvSeq s = kv_seq(rows, b);
   if (!s.ok) {

@@ -30,8 +30,7 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
   extern __shared__ double s_q[];  // [G][NC][8 dims of a piece][8 lanes]
   __shared__ int s_phys[kScoreChunk];
   __shared__ KvRow at;
-  pdl_wait();
-  pdl_trigger();
+  pdl_wait();  // (no early trigger: the next kernel's shared memory would leave these loads next to no L1)
   if (blockIdx.x == 0 && blockIdx.y == 0) kv_report_bad(rows, ctl, 5);
   const int m = blockIdx.x / Hkv, h = blockIdx.x - m * Hkv;
   for (int x = threadIdx.x; x < G * HD; x += kScoreThreads) {
