@@ -59,6 +59,10 @@ struct KvGeom {
   }
 };
 
+// These kernels are launched so that they may start while the kernel before them finishes (launch_pdl):
+// what they read may still be being written then, so after pdl_wait() it is read by ordinary loads, never
+// by non-coherent ones.
+
 // The ragged batch of a call (gpt_kv_batch), with the number of rows of the row tensors.
 struct KvRows {
   const int* table;

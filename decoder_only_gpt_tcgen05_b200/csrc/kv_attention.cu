@@ -363,10 +363,10 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
       for (int wi = 0; wi < KW; ++wi) {
         const __nv_bfloat16* src = p.q + row * HD + 4 * PER * wi + PER * c;
         if (G::BITS == 4) {
-          const uint4 v = row >= 0 ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          const uint4 v = row >= 0 ? *reinterpret_cast<const uint4*>(src) : make_uint4(0, 0, 0, 0);
           xw[4 * wi] = v.x, xw[4 * wi + 1] = v.y, xw[4 * wi + 2] = v.z, xw[4 * wi + 3] = v.w;
         } else {
-          const uint2 v = row >= 0 ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0, 0);
+          const uint2 v = row >= 0 ? *reinterpret_cast<const uint2*>(src) : make_uint2(0, 0);
           xw[2 * wi] = v.x, xw[2 * wi + 1] = v.y;
         }
       }

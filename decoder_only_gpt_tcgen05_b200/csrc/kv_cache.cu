@@ -421,8 +421,8 @@ kv_append_kernel(const __nv_bfloat16* __restrict__ qkv, KvRows rows, int blocks_
 // a float by setting it into the low bits of 2^23.
 template <class G>
 __global__ void __launch_bounds__(256)
-kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tiles, int n_blocks, int Hkv,
-               __nv_bfloat16* __restrict__ k_out, __nv_bfloat16* __restrict__ v_out, DevCtl ctl) {
+kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* tiles, int n_blocks, int Hkv,
+               __nv_bfloat16* k_out, __nv_bfloat16* v_out, DevCtl ctl) {
   constexpr int HD = G::HD;
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int h = blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -456,7 +456,7 @@ kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tile
       const uint8_t* rec = tile + slot / kKvRec * G::REC;
 #pragma unroll
       for (int p = 0; p < G::VB / 4; ++p) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16));
+        const uint4 x = *reinterpret_cast<const uint4*>(rec + G::VCODES + i0 * G::ROWB + p * 512 + lane * 16);
         uv[n][4 * p] = x.x, uv[n][4 * p + 1] = x.y, uv[n][4 * p + 2] = x.z, uv[n][4 * p + 3] = x.w;
       }
 #pragma unroll
@@ -465,17 +465,17 @@ kv_read_kernel(KvRows rows, int blocks_per_seq, const uint8_t* __restrict__ tile
         for (int p = 0; p < G::KB / G::KP; ++p) {
           const uint8_t* at = rec + i0 * G::ROWB + p * 64 * G::KP + (r + 8 * hf) * 4 * G::KP + c * G::KP;
           if (G::KP == 16) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 x = *reinterpret_cast<const uint4*>(at);
             uk[n][hf][4 * p] = x.x, uk[n][hf][4 * p + 1] = x.y, uk[n][hf][4 * p + 2] = x.z, uk[n][hf][4 * p + 3] = x.w;
           } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2*>(at));
+            const uint2 x = *reinterpret_cast<const uint2*>(at);
             uk[n][hf][0] = x.x, uk[n][hf][1] = x.y;
           }
         }
       auto scales = [&](int off, int i) -> unsigned int {
         const uint8_t* at = rec + off + (i0 + i) * 2 * G::NG;
-        return G::NG == 2 ? __ldg(reinterpret_cast<const unsigned int*>(at))
-                          : __ldg(reinterpret_cast<const unsigned short*>(at));
+        return G::NG == 2 ? *reinterpret_cast<const unsigned int*>(at)
+                          : *reinterpret_cast<const unsigned short*>(at);
       };
 #pragma unroll
       for (int sl = 0; sl < 4; ++sl) sv[n][sl] = scales(G::VSCALE, 2 * c + (sl & 1) + 8 * (sl >> 1));
@@ -584,8 +584,10 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   const int Hkv = cache->n_kv_head;
   if (H < 1 || H % Hkv) return set_error(ST_INVALID_ARG, "kv_append: H must be a multiple of n_kv_head");
   if ((long long)H + 2LL * Hkv > 65536) return set_error(ST_UNSUPPORTED, "kv_append: more than 65536 heads");
-  if (rope && !(rope_base > 1.f)) return set_error(ST_INVALID_ARG, "kv_append: rope_base must be > 1");
-  if (qk_norm && !(eps > 0.f)) return set_error(ST_INVALID_ARG, "kv_append: eps must be > 0");
+  if (rope && !(rope_base > 1.f && std::isfinite(rope_base)))
+    return set_error(ST_INVALID_ARG, "kv_append: rope_base must be finite and > 1");
+  if (qk_norm && !(eps > 0.f && std::isfinite(eps)))
+    return set_error(ST_INVALID_ARG, "kv_append: eps must be finite and > 0");
   if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
   if (!qkv || !q_out) return set_error(ST_INVALID_ARG, "kv_append: null qkv or q_out");
   if (misaligned(qkv, 16) || misaligned(q_out, 16))
@@ -594,6 +596,8 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   const long long bps = ((long long)max_new + kKvBlock - 2) / kKvBlock + 1;  // blocks that max_new tokens can touch
   if (bps * batch->n_seq > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_append: n_seq x max_new too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const DevCtl ctl = device_ctl();
+  if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   RopeFreq f;
   for (int i = 0; i < 64; ++i)
     f.f[i] = rope ? std::pow((double)rope_base, -2.0 * i / cache->head_dim) : 0.0;
@@ -619,7 +623,7 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     GPTK_CUDA(launch_pdl(kv_append_kernel<G>, dim3((unsigned)ctas, (unsigned)y), dim3(kAppendThreads), SMEM, st,
                          static_cast<const __nv_bfloat16*>(qkv), r, (int)bps, static_cast<uint8_t*>(cache->tiles),
                          static_cast<__nv_bfloat16*>(cache->bounds), (int)cache->n_blocks, H, Hkv, rope, qk_norm, eps, f,
-                         static_cast<__nv_bfloat16*>(q_out), device_ctl()));
+                         static_cast<__nv_bfloat16*>(q_out), ctl));
     return ST_OK;
   });
 }
@@ -638,6 +642,8 @@ GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch,
   if (bps * batch->n_seq > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_read: n_seq x max_new too large");
   const int groups = (Hkv + 7) / 8, warps = (Hkv + groups - 1) / groups;  // heads spread evenly over the CTAs
   if (groups > 65535) return set_error(ST_UNSUPPORTED, "kv_read: too many kv heads");
+  const DevCtl ctl = device_ctl();
+  if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   Prof prof(PK_MISC, 0, (double)M * Hkv * cache->head_dim * (4 + cache->bits / 4.0), st);
   return kv_dispatch(cache, [&](auto g) -> int {
@@ -646,7 +652,7 @@ GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch,
     r.max_new = max_new;
     GPTK_CUDA(launch_pdl(kv_read_kernel<G>, dim3((unsigned)(bps * batch->n_seq), (unsigned)groups), dim3(32 * warps), 0,
                          st, r, (int)bps, static_cast<const uint8_t*>(cache->tiles), (int)cache->n_blocks, Hkv,
-                         static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), device_ctl()));
+                         static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), ctl));
     return ST_OK;
   });
 }

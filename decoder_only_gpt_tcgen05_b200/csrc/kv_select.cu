@@ -24,8 +24,8 @@ constexpr int kScoreChunk = 64;  // blocks a CTA scores: two turns, whose loads 
 // chosen first), two where several share them.
 template <int HD, bool ONE>
 __global__ void __launch_bounds__(kScoreThreads)
-kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfloat16* __restrict__ bounds,
-                int n_blocks, int G, int Hkv, float* __restrict__ scores, DevCtl ctl) {
+kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds,
+                int n_blocks, int G, int Hkv, float* scores, DevCtl ctl) {
   constexpr int NC = HD / 64;
   extern __shared__ double s_q[];  // [G][NC][8 dims of a piece][8 lanes]
   __shared__ int s_phys[kScoreChunk];
@@ -68,8 +68,8 @@ kv_score_kernel(const __nv_bfloat16* __restrict__ q, KvRows rows, const __nv_bfl
     const uint4* p = reinterpret_cast<const uint4*>(bounds + ((long long)phys * Hkv + h) * 2 * HD);
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      lo[i][c] = live ? __ldg(p + c * 8 + l) : make_uint4(0, 0, 0, 0);
-      hi[i][c] = live ? __ldg(p + HD / 8 + c * 8 + l) : make_uint4(0, 0, 0, 0);
+      lo[i][c] = live ? p[c * 8 + l] : make_uint4(0, 0, 0, 0);
+      hi[i][c] = live ? p[HD / 8 + c * 8 + l] : make_uint4(0, 0, 0, 0);
     }
   }
 #pragma unroll
@@ -128,8 +128,8 @@ __device__ __forceinline__ unsigned int pick_key(float v, int j, int nb, int n_f
 }
 
 __global__ void __launch_bounds__(kPickThreads)
-kv_pick_kernel(const float* __restrict__ scores, KvRows rows, int Hkv, int n, int n_first, int n_last,
-               int* __restrict__ blocks) {
+kv_pick_kernel(const float* scores, KvRows rows, int Hkv, int n, int n_first, int n_last,
+               int* blocks) {
   __shared__ int hist[256];
   __shared__ unsigned int s_key[kPickKeys];
   __shared__ KvRow at;
@@ -236,6 +236,8 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
       (reinterpret_cast<uintptr_t>(scores) & 3))
     return set_error(ST_INVALID_ARG, "kv_select: q must be 16-byte, blocks and scores 4-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const DevCtl ctl = device_ctl();
+  if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   KvRows r = kv_rows(batch, M);
   if (!batch->cu_new) r.max_new = 1;
   const int hd = cache->head_dim;
@@ -247,7 +249,7 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     auto* qp = static_cast<const __nv_bfloat16*>(q);
     auto go = [&](auto kern) {
       return launch_pdl(kern, grid, dim3(kScoreThreads), smem, st, qp, r, bp, (int)cache->n_blocks, G, Hkv, scores,
-                        device_ctl());
+                        ctl);
     };
     GPTK_CUDA(hd == 64 ? (G == 1 ? go(kv_score_kernel<64, true>) : go(kv_score_kernel<64, false>))
                        : (G == 1 ? go(kv_score_kernel<128, true>) : go(kv_score_kernel<128, false>)));

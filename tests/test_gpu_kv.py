@@ -13,6 +13,10 @@ Tolerances, from the roundings the kernels make:
     accumulated sums hold p scale (code - Z) as differences of terms up to p scale 2 Z, 2^-20 of
     those; and the output is bf16, 2^-8 |o|.  lse: e_s + 2^-21 (1 + |lse|).
   - block scores: fp64 sums rounded to fp32, 2^-24; chosen blocks: equal."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -22,6 +26,7 @@ import synth
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def _g():
@@ -606,6 +611,49 @@ def test_attention_over_a_list_of_the_callers_own():
     check_attend(w, [2, 1], f64(q), f64(o), f64(lse), sel=sel)
 
 
+def test_selection_of_many_rows_and_many_blocks():
+    """More rows than a CTA scans by itself; more blocks than the choice keeps in shared memory.  Blocks
+    may recur in a table: 5000 entries over five cache blocks, so that most scores are ties."""
+    rng = np.random.default_rng(9)
+    lens = [int(x) for x in rng.integers(0, 200, 600)]
+    new = [min(1 + b % 2, n) for b, n in enumerate(lens)]
+    w = World(8, 64, 1, lens, 73)
+    batch, cu = w.batch(new, max_new=2)
+    M = sum(new)
+    q = bf(normal((M, 128), 4))
+    blocks, scores = w.cache.select(batch, q, 2, n_first=0, n_last=1)
+    o, lse = w.cache.attend(batch, q, blocks=blocks)
+    _g().model.sync_status(DEV)
+    got, sc = blocks.cpu().numpy(), f64(scores)
+    for b, m0 in enumerate(cu[:-1]):
+        for i in range(new[b]):
+            nb = (lens[b] - new[b] + i) // 64 + 1
+            want = O.kv.choose(sc[m0 + i, 0, :nb], 2, 0, 1)
+            assert got[m0 + i, 0].tolist() == want + [-1] * (2 - len(want))
+    check_attend(w, new, f64(q), f64(o), f64(lse), sel=got)
+
+    w = World(4, 64, 2, [64 * 5], 74)
+    W = 5000
+    at = rng.integers(0, 5, W)
+    table = w.table[0, at][None]
+    n = W * 64 - 20
+    batch = _g().KVBatch(i32(table), i32([n]))
+    q = bf(normal((1, 256), 5))
+    blocks, scores = w.cache.select(batch, q, 300, n_first=2, n_last=3)
+    sc = f64(scores)[0]
+    for h in range(2):
+        assert blocks[0, h].tolist() == O.kv.choose(sc[h], 300, 2, 3)
+    o, lse = w.cache.attend(batch, q)
+    _g().model.sync_status(DEV)
+    # 320k keys, as 320 with the number of times that each occurs
+    times = np.repeat(np.bincount(at, minlength=5), 64).astype(float)
+    times[at[-1] * 64 + 44:at[-1] * 64 + 64] -= 1
+    wt = np.repeat(times[None], 2, 0)
+    ro, rl, av = O.kv.attend(f64(q)[0].reshape(4, 64), w.k[0], w.v[0], wt)
+    to, tl = attend_bounds(w, 0, f64(q)[0].reshape(4, 64), ro, rl, av, wt)
+    assert np.all(np.abs(f64(o)[0].reshape(4, 64) - ro) <= to) and np.all(np.abs(f64(lse)[0] - rl) <= tl)
+
+
 # ---------------------------------------------------------------------------- together
 
 @pytest.mark.parametrize("bits,hd,H,Hkv", [(8, 128, 2, 2), (4, 64, 4, 2)])
@@ -708,6 +756,62 @@ def test_calls_on_two_streams_at_once():
     for i in range(2):
         for o, lse in got[i]:
             assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_two_captured_graphs_replay_at_once():
+    """Each capture has scratch of its own: two graphs on two streams do not disturb one another."""
+    w = World(8, 128, 2, [1500, 900, 2000], 83)
+    batch, _ = w.batch([1, 1, 1])
+    qs = [bf(normal((3, 256), s)) for s in (4, 5)]
+    want = [[t.clone() for t in w.cache.attend(batch, q)] for q in qs]
+    torch.cuda.synchronize()
+    graphs, outs, streams = [], [], [torch.cuda.Stream(DEV) for _ in qs]
+    for q in qs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(w.cache.attend(batch, q))
+        graphs.append(g)
+    for _ in range(20):
+        for o, lse in outs:
+            o.zero_(), lse.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for (o, lse), (ro, rl) in zip(outs, want):
+            assert torch.equal(o, ro) and torch.equal(lse, rl)
+
+
+def test_first_call_of_a_process_may_be_captured():
+    code = ("import torch, decoder_only_gpt_tcgen05_b200 as g\n"
+            "d = torch.device('cuda:0')\n"
+            "c = g.KVCache(4, 2, 128, bits=4, device=d)\n"
+            "b = g.KVBatch(torch.tensor([[1, 3]], dtype=torch.int32, device=d), torch.tensor([70], dtype=torch.int32, device=d))\n"
+            "x = torch.randn(1, 6 * 128, device=d).bfloat16()\n"
+            "torch.cuda.synchronize()\n"
+            "h = torch.cuda.CUDAGraph()\n"
+            "with torch.cuda.graph(h):\n"
+            "    q = c.append(b, x, 2); s = c.select(b, q, 2); o = c.attend(b, q, blocks=s[0]); k = c.read(b, 1)\n"
+            "h.replay(); torch.cuda.synchronize(); g.model.sync_status(d)\n"
+            "q2 = c.append(b, x, 2); o2 = c.attend(b, q2, blocks=c.select(b, q2, 2)[0])\n"
+            "assert torch.equal(o[0], o2[0]) and torch.equal(q, q2) and torch.isfinite(o[1]).all()\n")
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_rows_before_the_first_sequence_and_sequences_without_new_tokens():
+    w = World(4, 128, 2, [100, 50, 300], 84)
+    batch = _g().KVBatch(i32(w.table), i32(w.lens), i32([4, 6, 6, 9]), max_new=7)
+    q = bf(normal((12, 256), 4))
+    for blocks in (None, torch.zeros((12, 2, 1), dtype=torch.int32, device=DEV)):
+        o, lse = torch.full_like(q, 7.0), torch.full((12, 2), 7.0, device=DEV)
+        w.cache.attend(batch, q, blocks=blocks, o=o, lse=lse)
+        _g().model.sync_status(DEV)
+        for t in (o, lse):
+            assert torch.all(t[:4] == 7.0) and torch.all(t[9:] == 7.0)
+        sel = None if blocks is None else np.zeros((5, 2, 1), int)
+        check_attend(w, [2, 0, 3], f64(q)[4:9], f64(o)[4:9], f64(lse)[4:9], sel=sel)
 
 
 def test_binding_refuses_wrong_tensors():
