@@ -599,8 +599,10 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   const DevCtl ctl = device_ctl();
   if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   RopeFreq f;
-  for (int i = 0; i < 64; ++i)
-    f.f[i] = rope ? std::pow((double)rope_base, -2.0 * i / cache->head_dim) : 0.0;
+  // powers of one ratio in extended precision: 64 calls of pow would take longer than the launch
+  long double fi = 1.0L;
+  const long double ratio = rope ? std::pow((long double)rope_base, -2.0L / cache->head_dim) : 0.0L;
+  for (int i = 0; i < 64; ++i, fi *= ratio) f.f[i] = (double)fi;
   const double row = (double)(H + 2 * Hkv) * cache->head_dim;
   Prof prof(PK_QK, 0, M * row * 2 + (double)M * H * cache->head_dim * 2, st);
   return kv_dispatch(cache, [&](auto g) -> int {

@@ -23,16 +23,23 @@ def tile_bytes(bits: int, head_dim: int) -> int:
     return n.value
 
 
+_device, _raw_stream = (getattr(torch._C, n, None) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream"))
+_calls = {}  # library functions by name
+
+
 def _launch(name: str, dev: torch.device, *args) -> None:
     """The library call ``name`` with ``dev``'s current stream as its last argument, launched on ``dev``
     whichever device is current.  A decoding step is a handful of calls of a few microseconds, so this
     path takes the raw stream handle and enters a device guard only where it changes something."""
-    f = getattr(lib(), name)
-    if torch._C._cuda_getDevice() == dev.index:
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(lib(), name)
+    i = dev.index
+    if _device() == i:
+        rc = f(*args, _raw_stream(i))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+            rc = f(*args, _raw_stream(i))
     if rc:
         check(rc)
 
