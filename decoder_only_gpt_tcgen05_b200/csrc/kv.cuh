@@ -103,13 +103,16 @@ struct KvRow {
 __device__ __forceinline__ void kv_find_row(const KvRows& r, int m, KvRow* at) {
   if (threadIdx.x == 0) at->b = -1;
   __syncthreads();
-  for (int b = r.cu ? threadIdx.x : m; b < r.B; b += blockDim.x) {
-    const bool mine = r.cu ? r.cu[b] <= m && m < r.cu[b + 1] : threadIdx.x == 0;
-    if (mine) {
-      const KvSeq s = kv_seq(r, b);
-      *at = KvRow{b, s.ok ? s.len - s.n + (m - s.row0) : -1};
+  if (!r.cu) {
+    if (threadIdx.x == 0 && m < r.B) {
+      const KvSeq s = kv_seq(r, m);
+      *at = KvRow{m, s.ok ? s.len - 1 : -1};
     }
-    if (!r.cu) break;
+  } else {
+    for (int b = threadIdx.x; b < r.B; b += blockDim.x) {
+      const KvSeq s = kv_seq(r, b);  // (its loads do not wait for one another)
+      if (s.row0 <= m && m < r.cu[b + 1]) *at = KvRow{b, s.ok ? s.len - s.n + (m - s.row0) : -1};
+    }
   }
   __syncthreads();
 }

@@ -76,6 +76,7 @@ kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds
   for (int i = 0; i < TURNS; ++i) {
     const int j = j0 + i * TURN + (threadIdx.x >> 3);
     double acc[4] = {0.0, 0.0, 0.0, 0.0};  // four chains: the fp64 add's latency is many cycles
+    // (the sign of q is read from its high word: a comparison would take the fp64 unit as well)
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
       const uint4 vl = lo[i][c], vh = hi[i][c];
@@ -91,7 +92,7 @@ kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
           const double qv = qp[x * 8];
-          acc[x % 4] = fma(qv, (double)(qv > 0.0 ? e[x] : a[x]), acc[x % 4]);
+          acc[x % 4] = fma(qv, (double)(__double2hiint(qv) >= 0 ? e[x] : a[x]), acc[x % 4]);
         }
       } else {
         double da[8], de[8];
@@ -102,7 +103,7 @@ kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds
 #pragma unroll
           for (int x = 0; x < 8; ++x) {
             const double qv = qp[g * HD + x * 8];
-            acc[x % 4] = fma(qv, qv > 0.0 ? de[x] : da[x], acc[x % 4]);
+            acc[x % 4] = fma(qv, __double2hiint(qv) >= 0 ? de[x] : da[x], acc[x % 4]);
           }
         }
       }
