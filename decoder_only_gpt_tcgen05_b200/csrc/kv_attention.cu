@@ -215,6 +215,8 @@ template <class G, int NT, int QC, bool SPARSE>
 __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>::CTAS) kv_attend_kernel(AttendArgs p) {
   using C = AttendCfg<G, NT>;
   constexpr int HD = G::HD, NG = G::NG, RT = 4 * QC * NT, MT = HD / 16, KW = G::KB / 4, VW = G::VB / 4;
+  // with one column used, a column pair's other half carries the weights of the second scale group
+  constexpr int PG = QC == 1 ? 1 : NG;  // operands P a key tile
   constexpr int U = C::U, TL = NT == 2 ? 1 : QC == 2 ? 2 : U / 16;  // keys of a unit; 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ uint64_t bars[C::WARPS][C::STAGES];
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         }
       }
       // probabilities, and times the value scale as the fp16 operand P^T[key][query]
-      unsigned int pb[TL][NG][NT][2];
+      unsigned int pb[TL][PG][NT][2];
 #pragma unroll
       for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
@@ -680,12 +682,15 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
               l[nt][q] += pr[q];
             }
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
+            for (int g = 0; g < PG; ++g) {
               float w[2] = {0.f, 0.f};
+              if (QC == 1) {
 #pragma unroll
-              for (int q = 0; q < QC; ++q) {
-                w[q] = pr[q] * sv[g];
-                if (edge && x[tl][nt][QC * hf + q] == -INFINITY) w[q] = 0.f;
+                for (int k = 0; k < NG; ++k) w[k] = edge && x[tl][nt][hf] == -INFINITY ? 0.f : pr[0] * sv[k];
+              } else {
+#pragma unroll
+                for (int q = 0; q < QC; ++q)
+                  w[q] = edge && x[tl][nt][QC * hf + q] == -INFINITY ? 0.f : pr[q] * sv[g];
               }
               pb[tl][g][nt][hf] = transpose8(pack_h2(w[0], w[1]));
             }
@@ -707,8 +712,9 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         }
 #pragma unroll
         for (int wj = 0; wj < VW; ++wj) {
-          const int g = NG == 1 ? 0 : wj;
-          if (wj == 0 || NG == 2) {
+          const int g = PG == 1 ? 0 : wj;       // operand P
+          const int k = QC == 1 && NG == 2 ? wj : 0;  // its column
+          if (wj == 0 || PG == 2) {
             constexpr unsigned int ZC = 0x80008000u | G::Z | (G::Z << 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -750,7 +756,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
                   mma_f16(d, x01[tl] & mask, second(x01[tl]), x23[tl] & mask, second(x23[tl]), pb[tl][g][nt]);
                 float(&o)[2 * QC] = acc[nt][G::BITS == 4 ? 4 * wj + 2 * part + z : 2 * wj + part];
                 if (QC == 1) {
-                  o[0] += d[0], o[1] += d[2];
+                  o[0] += d[k], o[1] += d[2 + k];
                 } else {
                   const float2 s0 = fadd2(make_float2(o[0], o[1]), make_float2(d[0], d[1]));
                   const float2 s1 = fadd2(make_float2(o[2 * QC - 2], o[2 * QC - 1]), make_float2(d[2], d[3]));
