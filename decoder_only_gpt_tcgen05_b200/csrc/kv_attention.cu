@@ -24,7 +24,8 @@
 //
 // Numbers: scores, maxima, sums and outputs are fp32; q is scaled by a power of two into fp16, which
 // is exact for a bf16 q down to 2^-28 of its row's largest; probabilities times the value scale are
-// rounded to fp16 (2^-11; four times finer than bf16's 2^-9, below the output's own rounding).
+// rounded to fp16: by 2^-11 of their size at most (bf16's step would be eight times that), or, those below
+// 2^-19 of the largest value scale that the worker has met, by 2^-30 of that scale.
 #include <cfloat>
 #include <cmath>
 #include <string>
@@ -209,15 +210,17 @@ struct AttendCfg {
 // uses the even ones alone, for tiles of at most four query rows (a step of a model without shared kv
 // heads has one), and leaves out half of the softmax's and the output's arithmetic and registers.  A
 // step then takes a whole unit (TL tiles), a record with all columns, half of one with two column tiles:
-// what fits the registers.  (32 sequences of 16k to 32k tokens in 4 bits: 212 us with both columns and a
-// record a step, 198 with one, 185 with one and 64 keys a step.)
+// what fits the registers (8 bits at 128 dims have one scale a row, which leaves room for a record: 16
+// prompts of 128 tokens 92.8 -> 89.1 us; at 64 dims it spills).  (32 sequences of 16k to 32k tokens in 4
+// bits: 212 us with both columns and a record a step, 198 with one, 185 with one and 64 keys a step.)
 template <class G, int NT, int QC, bool SPARSE>
 __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>::CTAS) kv_attend_kernel(AttendArgs p) {
   using C = AttendCfg<G, NT>;
   constexpr int HD = G::HD, NG = G::NG, RT = 4 * QC * NT, MT = HD / 16, KW = G::KB / 4, VW = G::VB / 4;
   // with one column used, a column pair's other half carries the weights of the second scale group
   constexpr int PG = QC == 1 ? 1 : NG;  // operands P a key tile
-  constexpr int U = C::U, TL = NT == 2 ? 1 : QC == 2 ? 2 : U / 16;  // keys of a unit; 16-key tiles of a step
+  constexpr int U = C::U;  // keys of a unit
+  constexpr int TL = NT == 2 ? (G::BITS == 8 && HD == 128 ? 2 : 1) : QC == 2 ? 2 : U / 16;  // 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ uint64_t bars[C::WARPS][C::STAGES];
   __shared__ int meta[C::WARPS][C::STAGES];
@@ -864,7 +867,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int
   if (mine && t.nrec > 0) {
     const long long total = (p.prefix[p.E] + (long long)kSegWeight * p.count[p.E]) * p.Hkv;
     const long long workers = min((long long)max_workers, total);
-    const long long at = (p.prefix[e] + (long long)kSegWeight * p.count[e]) * p.Hkv + h * (t.nrec + kSegWeight) + kSegWeight;
+    const long long at = (p.prefix[e] + (long long)kSegWeight * p.count[e]) * p.Hkv +
+                         (long long)h * (t.nrec + kSegWeight) + kSegWeight;
     w0 = worker_of(at, total, workers);
     w1 = worker_of(at + t.nrec - 1, total, workers);
     mine = w0 != w1;  // else one worker had all of it

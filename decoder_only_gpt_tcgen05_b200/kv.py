@@ -165,7 +165,8 @@ class KVCache:
     def attend(self, batch: KVBatch, q: torch.Tensor, *, window: int = -1, blocks: torch.Tensor | None = None,
                o: torch.Tensor | None = None, lse: torch.Tensor | None = None, scratch: torch.Tensor | None = None):
         """(o bf16 [M, n_head head_dim], lse fp32 [M, n_head]): attention of the new tokens over the cache,
-        over all earlier keys, over the last ``window`` and itself, or over the listed ``blocks``.
+        over all earlier keys, over the last ``window`` and itself, or over the listed ``blocks`` (of each
+        list the first min(length, visible blocks) entries are read: put the visible ones first).
         ``scratch`` (uint8, scratch_bytes) may be passed in; calls that overlap need their own."""
         M, H = q.shape[0], self._heads(q)
         _check(q, "q", torch.bfloat16, self.device)

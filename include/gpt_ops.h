@@ -258,7 +258,7 @@ GPT_API int gpt_kv_tile_bytes(int bits, int head_dim, size_t* bytes);
  * block whose first token is among the new ones starts afresh, otherwise the
  * new keys widen what was there (so writing a position again may leave them
  * wider than need be, never narrower).
- * Two sequences of one call must not write to the same block. */
+ * No block may be written under two entries of one call's block tables. */
 GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batch, const void* qkv, int M, int H,
                              int rope, int qk_norm, float rope_base, float eps, void* q_out, void* stream);
 
