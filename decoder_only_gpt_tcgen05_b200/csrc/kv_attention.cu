@@ -34,6 +34,20 @@
 
 namespace gptk {
 
+// x / d for 0 <= x < 2^31 as a product and a shift, exact: m = (2^s + e) / d with e < d <= 2^(s - 31), so
+// that x e / d < 2^s / d.  (The starts of these kernels are chains of such divisions, 100 clocks each
+// otherwise.)
+struct KvDiv {
+  unsigned int m;
+  int s;
+  __host__ explicit KvDiv(int d = 1) {
+    s = 31;
+    while ((1LL << (s - 31)) < d) ++s;
+    m = (unsigned int)(((1ULL << s) + d - 1) / d);
+  }
+  __device__ __forceinline__ int operator()(int x) const { return (int)(((unsigned long long)(unsigned int)x * m) >> s); }
+};
+
 struct AttendArgs {
   const __nv_bfloat16* q;
   const uint8_t* tiles;
@@ -43,6 +57,9 @@ struct AttendArgs {
   unsigned int block_bytes;  // of all kv heads' tiles
   int E, QT;       // entries, and tiles of query rows a sequence (sparse: a token) has
   int RV;          // query rows of a tile that can be in use (scratch rows)
+  KvDiv by_qt, by_g, by_rv, by_hkv;  // x / QT, G, RV, Hkv
+  int max_workers;
+  unsigned long long worker_m;  // 2^64 / max_workers, rounded up
   int scanned;     // 1: prefix already holds the units before each entry (E large)
   float scale_log2;
   __nv_bfloat16* o;
@@ -71,7 +88,7 @@ struct KvSpan {
 template <bool SPARSE>
 __device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, int U, bool report) {
   KvEntry t;
-  const int unit = e / p.QT;
+  const int unit = p.by_qt(e);
   t.rho0 = (e - unit * p.QT) * RT;
   t.nrows = t.nrec = t.jlo = t.nb = t.pos0 = t.row0 = 0;
   t.b = unit;
@@ -97,7 +114,7 @@ __device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, 
   t.nrows = min(RT, total - t.rho0);
   t.row0 = SPARSE ? unit : s.row0;
   t.pos0 = SPARSE ? s.len - s.n + (unit - s.row0) : s.len - s.n;
-  const int lo = t.pos0 + t.rho0 / p.G, hi = t.pos0 + (t.rho0 + t.nrows - 1) / p.G;
+  const int lo = t.pos0 + p.by_g(t.rho0), hi = t.pos0 + p.by_g(t.rho0 + t.nrows - 1);
   if (SPARSE) {
     t.nb = lo / kKvBlock + 1;
     t.nrec = kKvBlock / U * min(p.n_sel, t.nb);
@@ -115,22 +132,78 @@ __device__ __forceinline__ KvEntry kv_entry(const AttendArgs& p, int e, int RT, 
 // Weight [w total / workers, (w + 1) total / workers) is worker w's; a segment's extra weight lies before
 // its first unit.
 constexpr int kSegWeight = 2;
-__device__ __forceinline__ long long worker_of(long long weight, long long total, long long workers) {
-  return ((weight + 1) * workers - 1) / total;
+// (64-bit division takes hundreds of clocks and is needed for huge batches only)
+__device__ __forceinline__ long long div_pos(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((unsigned int)a / (unsigned int)b) : a / b;
 }
-// units of all heads before weight v: pre and cnt are the units of one head, and the non-empty entries,
-// before each entry
-__device__ __forceinline__ long long units_before(const long long* pre, const int* cnt, int E, int Hkv, long long v) {
-  int lo = 0, hi = E;  // last entry whose weight begins at or before v
+__device__ __forceinline__ long long worker_of(long long weight, long long total, long long workers) {
+  return div_pos((weight + 1) * workers - 1, total);
+}
+// w total / workers for workers = min(max_workers, total): by the reciprocal, exact while
+// w total max_workers < 2^64, which is far beyond any batch that fits
+__device__ __forceinline__ long long share_begin(const AttendArgs& p, int w, long long total) {
+  return total <= p.max_workers ? w : (long long)__umul64hi((unsigned long long)w * total, p.worker_m);
+}
+// The first unit at or after weight v: its entry, head and number there, and how many units of all heads lie
+// before it.  pre and cnt are the units of one head, and the non-empty entries, before each entry.
+struct KvPlace {
+  long long unit;
+  int e, h, j;
+};
+__device__ __forceinline__ KvPlace unit_at(const long long* pre, const int* cnt, int E, int Hkv, long long v) {
+  int lo = 0, hi = E;  // last entry whose weight begins at or before v: not an empty one, unless v is the end
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if ((pre[mid] + (long long)kSegWeight * cnt[mid]) * Hkv <= v) lo = mid;
     else hi = mid;
   }
   const long long n = pre[lo + 1] - pre[lo], r = v - (pre[lo] + (long long)kSegWeight * cnt[lo]) * Hkv;
-  if (n == 0) return pre[lo] * Hkv;  // (v is the end of all)
-  const long long h = min(r / (n + kSegWeight), (long long)Hkv), j = r - h * (n + kSegWeight);
-  return pre[lo] * Hkv + h * n + max(0LL, j - kSegWeight);
+  KvPlace at;
+  at.e = lo;
+  at.h = n == 0 ? 0 : (int)min(div_pos(r, n + kSegWeight), (long long)Hkv);
+  at.j = max(0, (int)(r - at.h * (n + kSegWeight)) - kSegWeight);
+  if (n == 0) at.j = 0;
+  at.unit = pre[lo] * Hkv + at.h * n + at.j;
+  return at;
+}
+
+// The units before each entry, by a whole block of W warps: into pre and cnt (and gpre and gcnt, unless
+// null).  Ends with a barrier.
+template <bool SPARSE, int W>
+__device__ __forceinline__ void kv_scan(const AttendArgs& p, int RT, int U, bool report, long long* s_warp, int* s_wcnt,
+                                        long long* pre, int* cnt, long long* gpre, int* gcnt) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  long long run = 0;
+  int runc = 0;
+  for (int e0 = 0; e0 < p.E; e0 += W * 32) {
+    const int e = e0 + tid;
+    long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, U, report).nrec : 0;
+    const long long own = v;
+    const unsigned int full = __ballot_sync(0xffffffffu, own > 0);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += x;
+    }
+    if (lane == 31) s_warp[warp] = v, s_wcnt[warp] = __popc(full);
+    __syncthreads();
+    long long before = run;
+    int beforec = runc + __popc(full & ((1u << lane) - 1));
+    for (int x = 0; x < W; ++x) {
+      if (x < warp) before += s_warp[x], beforec += s_wcnt[x];
+      run += s_warp[x], runc += s_wcnt[x];
+    }
+    if (e < p.E) {
+      pre[e] = before + v - own, cnt[e] = beforec;
+      if (gpre) gpre[e] = before + v - own, gcnt[e] = beforec;
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    pre[p.E] = run, cnt[p.E] = runc;
+    if (gpre) gpre[p.E] = run, gcnt[p.E] = runc;
+  }
+  __syncthreads();
 }
 
 // d = A B + c
@@ -249,64 +322,24 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   const int* cnt = p.count;
   if (!p.scanned) {
     pre = s_pre, cnt = s_cnt;
-    long long run = 0;
-    int runc = 0;
-    for (int e0 = 0; e0 < p.E; e0 += C::WARPS * 32) {
-      const int e = e0 + tid;
-      long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, U, blockIdx.x == 0).nrec : 0;
-      const long long own = v;
-      const unsigned int full = __ballot_sync(0xffffffffu, own > 0);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += x;
-      }
-      if (lane == 31) s_warp[warp] = v, s_wcnt[warp] = __popc(full);
-      __syncthreads();
-      long long before = run;
-      int beforec = runc + __popc(full & ((1u << lane) - 1));
-      for (int x = 0; x < C::WARPS; ++x) {
-        if (x < warp) before += s_warp[x], beforec += s_wcnt[x];
-        run += s_warp[x], runc += s_wcnt[x];
-      }
-      if (e < p.E) {
-        s_pre[e] = before + v - own, s_cnt[e] = beforec;
-        if (blockIdx.x == 0) p.prefix[e] = before + v - own, p.count[e] = beforec;
-      }
-      __syncthreads();
-    }
-    if (tid == 0) {
-      s_pre[p.E] = run, s_cnt[p.E] = runc;
-      if (blockIdx.x == 0) p.prefix[p.E] = run, p.count[p.E] = runc;
-    }
+    const bool first = blockIdx.x == 0;
+    kv_scan<SPARSE, C::WARPS>(p, RT, U, first, s_warp, s_wcnt, s_pre, s_cnt, first ? p.prefix : nullptr, p.count);
+  } else {
+    __syncthreads();
   }
-  __syncthreads();
 
   // ---- this warp's share
   const long long total = (pre[p.E] + (long long)kSegWeight * cnt[p.E]) * p.Hkv;
-  const long long workers = min((long long)gridDim.x * C::WARPS, total);
   const int w = warp * gridDim.x + blockIdx.x;  // neighbours on different SMs
-  if (w >= workers) return;
+  if (w >= total) return;  // (there are max_workers warps)
   // (the even lanes find its beginning, the odd ones its end)
-  const long long bound = units_before(pre, cnt, p.E, p.Hkv, (w + (lane & 1)) * total / workers);
-  const long long ua = __shfl_sync(0xffffffffu, bound, 0);
-  const int units = (int)(__shfl_sync(0xffffffffu, bound, 1) - ua);
+  const KvPlace place = unit_at(pre, cnt, p.E, p.Hkv, share_begin(p, w + (lane & 1), total));
+  const int units = (int)(__shfl_sync(0xffffffffu, place.unit, 1) - __shfl_sync(0xffffffffu, place.unit, 0));
   if (units == 0) return;
 
   // ---- the fetching iterator, C::STAGES units ahead of the computing one
-  int fe, fh, fj;
-  {
-    int lo = 0, hi = p.E;  // last entry that starts at or before ua and is not empty
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pre[mid] * p.Hkv <= ua) lo = mid;
-      else hi = mid;
-    }
-    fe = lo;
-    const long long n = pre[fe + 1] - pre[fe], r = ua - pre[fe] * p.Hkv;
-    fh = (int)(r / n);
-    fj = (int)(r - fh * n);
-  }
+  int fe = __shfl_sync(0xffffffffu, place.e, 0), fh = __shfl_sync(0xffffffffu, place.h, 0);
+  int fj = __shfl_sync(0xffffffffu, place.j, 0);
   int j = fj;  // the computing iterator's unit; its entry and head are in sp
   KvSpan& sp = s_span[warp];
   const KvEntry& ft = s_fent[warp];
@@ -386,11 +419,11 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
     const KvEntry t = s_ent[warp];
     if (lane == 0) {
       sp.j_first = j;
-      sp.p_lo = t.pos0 + t.rho0 / p.G;
-      sp.p_hi = t.pos0 + (t.rho0 + t.nrows - 1) / p.G;
+      sp.p_lo = t.pos0 + p.by_g(t.rho0);
+      sp.p_hi = t.pos0 + p.by_g(t.rho0 + t.nrows - 1);
     }
     if (lane < RT) {  // the tile's query rows: position and row of q and o (-1: none)
-      const int tok = (t.rho0 + lane) / p.G, g = t.rho0 + lane - tok * p.G;
+      const int tok = p.by_g(t.rho0 + lane), g = t.rho0 + lane - tok * p.G;
       s_pos[warp][lane] = lane < t.nrows ? t.pos0 + tok : -1;
       s_row[warp][lane] = lane < t.nrows ? (long long)(t.row0 + tok) * p.H + sp.h * p.G + g : -1;
     }
@@ -812,31 +845,7 @@ __global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT, int 
   __shared__ int s_wcnt[8];
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  long long run = 0;
-  int runc = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 256) {
-    const int e = e0 + tid;
-    long long v = e < p.E ? kv_entry<SPARSE>(p, e, RT, U, true).nrec : 0;
-    const long long own = v;
-    const unsigned int full = __ballot_sync(0xffffffffu, own > 0);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += x;
-    }
-    if (lane == 31) s_warp[warp] = v, s_wcnt[warp] = __popc(full);
-    __syncthreads();
-    long long before = run;
-    int beforec = runc + __popc(full & ((1u << lane) - 1));
-    for (int x = 0; x < 8; ++x) {
-      if (x < warp) before += s_warp[x], beforec += s_wcnt[x];
-      run += s_warp[x], runc += s_wcnt[x];
-    }
-    if (e < p.E) p.prefix[e] = before + v - own, p.count[e] = beforec;
-    __syncthreads();
-  }
-  if (tid == 0) p.prefix[p.E] = run, p.count[p.E] = runc;
+  kv_scan<SPARSE, 8>(p, RT, U, true, s_warp, s_wcnt, p.prefix, p.count, nullptr, nullptr);
 }
 
 // Joins the parts of the query rows that were cut between workers, in the workers' order, and writes the
@@ -845,34 +854,46 @@ __global__ void __launch_bounds__(256) kv_scan_kernel(AttendArgs p, int RT, int 
 // so each step's loads are issued together: the row's place from the batch's own arrays before the
 // parts are waited for, then four parts with their logsumexps at a time.
 constexpr int kJoinThreads = 256;
+constexpr unsigned int kJoinScanCtas = 2 * 148;  // (with 4 x 148 the last of a larger grid scan too late: drafts 21.3 -> 22.3 us)
 template <int HD, bool SPARSE, int WPR>
-__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int U, int max_workers, int rows) {
+__global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int RT, int U, int rows) {
   constexpr int V = HD / 32;  // dims of a lane
   constexpr int W = kJoinThreads / 32;
   __shared__ float s_m[W], s_l[W];
   __shared__ float s_o[W][HD];
+  __shared__ long long s_pre[kScanSmem + 1], s_warp[W];
+  __shared__ int s_cnt[kScanSmem + 1], s_wcnt[W];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % WPR;
   const int row = blockIdx.x * (W / WPR) + warp / WPR;
-  const int seg = row / p.RV, n = row - seg * p.RV;
-  const int e = seg / p.Hkv, h = seg - e * p.Hkv;
-  // the batch's arrays are older than the kernel before this one, which has waited for them
+  const int seg = p.by_rv(row), n = row - seg * p.RV;
+  const int e = p.by_hkv(seg), h = seg - e * p.Hkv;
+  // The batch's arrays are older than the kernel before this one, which has waited for them.  A grid of one
+  // wave scans them again meanwhile; a larger one reads what that kernel has left (loads on its critical path).
   KvEntry t;
   t.nrows = 0;
   if (row < rows) t = kv_entry<SPARSE>(p, e, RT, U, false);
+  const bool scan = !p.scanned && gridDim.x <= kJoinScanCtas;
+  bool mine = n < t.nrows;
+  long long w0 = 0, w1 = -1;
+  auto locate = [&](const long long* pre, const int* cnt) {
+    if (mine && t.nrec > 0) {
+      const long long total = (pre[p.E] + (long long)kSegWeight * cnt[p.E]) * p.Hkv;
+      const long long workers = min((long long)p.max_workers, total);
+      const long long at =
+          (pre[e] + (long long)kSegWeight * cnt[e]) * p.Hkv + (long long)h * (t.nrec + kSegWeight) + kSegWeight;
+      w0 = worker_of(at, total, workers);
+      w1 = worker_of(at + t.nrec - 1, total, workers);
+      mine = w0 != w1;  // else one worker had all of it
+    }
+  };
+  if (scan) {
+    kv_scan<SPARSE, W>(p, RT, U, false, s_warp, s_wcnt, s_pre, s_cnt, nullptr, nullptr);
+    locate(s_pre, s_cnt);
+  }
   pdl_wait();
   pdl_trigger();
   if (SPARSE && blockIdx.x == 0) kv_report_bad(p.rows, p.ctl, 9);
-  bool mine = n < t.nrows;
-  long long w0 = 0, w1 = -1;
-  if (mine && t.nrec > 0) {
-    const long long total = (p.prefix[p.E] + (long long)kSegWeight * p.count[p.E]) * p.Hkv;
-    const long long workers = min((long long)max_workers, total);
-    const long long at = (p.prefix[e] + (long long)kSegWeight * p.count[e]) * p.Hkv +
-                         (long long)h * (t.nrec + kSegWeight) + kSegWeight;
-    w0 = worker_of(at, total, workers);
-    w1 = worker_of(at + t.nrec - 1, total, workers);
-    mine = w0 != w1;  // else one worker had all of it
-  }
+  if (!scan) locate(p.prefix, p.count);
   if (!mine && WPR == 1) return;
   if (WPR == W && !mine) return;  // the whole block
   float acc[V], sum = 0.f, mx = -INFINITY;
@@ -931,8 +952,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv_join_kernel(AttendArgs p, int
     }
   }
   const float ref = mx == -INFINITY ? 0.f : mx;
-  const int rho = t.rho0 + n;
-  const long long qrow = (long long)(t.row0 + rho / p.G) * p.H + (long long)h * p.G + rho % p.G;
+  const int rho = t.rho0 + n, tok = p.by_g(rho);
+  const long long qrow = (long long)(t.row0 + tok) * p.H + h * p.G + rho - tok * p.G;
   const float f = sum == 0.f ? 0.f : 1.f / sum;
   __nv_bfloat16* out = p.o + qrow * HD + lane * V;
 #pragma unroll
@@ -979,7 +1000,7 @@ static int attend_plan(const char* what, const gpt_kv_cache* c, const gpt_kv_bat
 }
 
 template <class G, int NT, int QC, bool SPARSE>
-static int launch_attend(const AttendArgs& a, const AttendPlan& pl, double bytes, double flops, cudaStream_t st) {
+static int launch_attend(AttendArgs a, const AttendPlan& pl, double bytes, double flops, cudaStream_t st) {
   using C = AttendCfg<G, NT>;
   auto kern = kv_attend_kernel<G, NT, QC, SPARSE>;
   static bool attr_set[64] = {};
@@ -991,6 +1012,8 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& pl, double bytes
   }
   int grid = num_sms() * C::CTAS;
   if (grid > kAttendMaxWorkers / C::WARPS) grid = kAttendMaxWorkers / C::WARPS;
+  a.max_workers = grid * C::WARPS;
+  a.worker_m = ~0ULL / a.max_workers + 1;
   if (a.scanned) {
     Prof prof(PK_ATTN_FWD, 0, 0, st);
     GPTK_CUDA(launch_pdl(kv_scan_kernel<SPARSE>, dim3(1), dim3(256), 0, st, a, pl.RT, (int)C::U));
@@ -1006,8 +1029,7 @@ static int launch_attend(const AttendArgs& a, const AttendPlan& pl, double bytes
   Prof prof(PK_ATTN_FWD, 0, 0, st);
   auto join = [&](auto kern, int wpr) {
     const unsigned int per = kJoinThreads / 32 / wpr;
-    return launch_pdl(kern, dim3((rows + per - 1) / per), dim3(kJoinThreads), 0, st, a, pl.RT, (int)C::U, (int)workers,
-                      rows);
+    return launch_pdl(kern, dim3((rows + per - 1) / per), dim3(kJoinThreads), 0, st, a, pl.RT, (int)C::U, rows);
   };
   GPTK_CUDA(parts >= 24  ? join(kv_join_kernel<G::HD, SPARSE, 8>, 8)
             : parts >= 6 ? join(kv_join_kernel<G::HD, SPARSE, 2>, 2)
@@ -1080,6 +1102,7 @@ GPT_API int gpt_op_attention_kv(const gpt_kv_cache* cache, const gpt_kv_batch* b
   a.E = (int)pl.E;
   a.QT = pl.QT;
   a.RV = pl.RV;
+  a.by_qt = KvDiv(a.QT), a.by_g = KvDiv(a.G), a.by_rv = KvDiv(a.RV), a.by_hkv = KvDiv(a.Hkv);
   a.scanned = pl.E > kScanSmem;
   a.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)cache->head_dim));
   a.o = static_cast<__nv_bfloat16*>(o);
