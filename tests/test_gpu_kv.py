@@ -611,6 +611,22 @@ def test_attention_over_a_list_of_the_callers_own():
     check_attend(w, [2, 1], f64(q), f64(o), f64(lse), sel=sel)
 
 
+@pytest.mark.parametrize("bits,hd,G,new", [(8, 128, 2, 12), (4, 64, 3, 7), (4, 128, 1, 3)])
+def test_many_short_sequences(bits, hd, G, new):
+    """More rows to join than a grid that scans the batch itself takes, fewer entries than need a scan of
+    their own; sequences of very different lengths, the shortest without a key of an earlier call."""
+    rng = np.random.default_rng(hd + G)
+    lens = [int(x) for x in rng.integers(1, 400, 90)]
+    lens[:3] = [0, 1, new]
+    n = [min(new, x) for x in lens]
+    w = World(bits, hd, 2, lens, 81)
+    batch, cu = w.batch(n, max_new=new)
+    q = bf(normal((cu[-1], 2 * G * hd), 5))
+    o, lse = w.cache.attend(batch, q)
+    _g().model.sync_status(DEV)
+    check_attend(w, n, f64(q), f64(o), f64(lse))
+
+
 def test_selection_of_many_rows_and_many_blocks():
     """More rows than a CTA scans by itself; more blocks than the choice keeps in shared memory.  Blocks
     may recur in a table: 5000 entries over five cache blocks, so that most scores are ties."""
