@@ -602,9 +602,11 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   const DevCtl ctl = device_ctl();
   if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   RopeFreq f;
-  // powers of one ratio in extended precision: 64 calls of pow would take longer than the launch
-  long double fi = 1.0L;
-  const long double ratio = rope ? std::pow((long double)rope_base, -2.0L / cache->head_dim) : 0.0L;
+  // powers of base^(-2 / hd), which is square roots of 1 / base, in extended precision (64 calls of pow would
+  // take longer than the launch; a table of 8 x 8 as a smaller parameter saves the host 0.6 us and costs 5 % of the
+  // kernel on prompts)
+  long double ratio = rope ? 1.0L / rope_base : 0.0L, fi = 1.0L;
+  for (int n = cache->head_dim / 2; n > 1; n /= 2) ratio = std::sqrt(ratio);
   for (int i = 0; i < 64; ++i, fi *= ratio) f.f[i] = (double)fi;
   const double row = (double)(H + 2 * Hkv) * cache->head_dim;
   Prof prof(PK_QK, 0, M * row * 2 + (double)M * H * cache->head_dim * 2, st);

@@ -51,11 +51,11 @@ def _check(t: torch.Tensor, name: str, dtype, dev, shape=None) -> None:
     assert shape is None or t.shape == shape, f"{name}: shape {tuple(shape)} needed, got {tuple(t.shape)}"
 
 
-def _out(t, name: str, shape, dtype, dev) -> torch.Tensor:
-    """The caller's output tensor, checked, or a new one."""
+def _out(t, name: str, shape, like: torch.Tensor) -> torch.Tensor:
+    """The caller's output tensor, checked, or a new one of ``like``'s type and device."""
     if t is None:
-        return torch.empty(*shape, dtype=dtype, device=dev)  # (sizes one by one: parsed faster than a tuple)
-    _check(t, name, dtype, dev, shape)
+        return like.new_empty(*shape)  # (sizes one by one: parsed faster than a tuple)
+    _check(t, name, like.dtype, like.device, shape)
     return t
 
 
@@ -76,7 +76,7 @@ class KVBatch:
             _check(cu_new, "cu_new", torch.int32, dev, (n + 1,))
         assert max_new >= 0 and (cu_new is not None or max_new == 1), "max_new: without cu_new it is 1"
         self.block_table, self.lens, self.cu_new, self.max_new, self.device = block_table, lens, cu_new, max_new, dev
-        self.n_seq = n
+        self.n_seq, self.max_blocks = n, w
         self._c = KVBatchParams(block_table.data_ptr(), lens.data_ptr(), cu_new.data_ptr() if cu_new is not None else None,
                                 n, w, max_new)
         self._ref = C.byref(self._c)
@@ -105,6 +105,9 @@ class KVCache:
         self.n_blocks, self.n_kv_head, self.head_dim, self.bits = n_blocks, n_kv_head, head_dim, bits
         self.tiles, self.bounds, self.device = tiles, bounds, dev
         self._scratch = {}
+        # what outputs are made like: a new tensor of the same type takes less time than one by type and device
+        self._bf16, self._f32, self._i32 = (torch.empty(0, dtype=t, device=dev)
+                                            for t in (torch.bfloat16, torch.float32, torch.int32))
         self._c = KVCacheParams(tiles.data_ptr(), bounds.data_ptr() if bounds is not None else None, n_blocks,
                                 n_kv_head, head_dim, bits)
         self._ref = C.byref(self._c)
@@ -116,10 +119,7 @@ class KVCache:
         M = qkv.shape[0]
         _check(qkv, "qkv", torch.bfloat16, self.device, (M, (n_head + 2 * self.n_kv_head) * self.head_dim))
         assert batch.device == self.device, "batch: on another device than the cache"
-        if q is None:
-            q = torch.empty(M, n_head * self.head_dim, dtype=torch.bfloat16, device=self.device)
-        else:
-            _check(q, "q", torch.bfloat16, self.device, (M, n_head * self.head_dim))
+        q = _out(q, "q", (M, n_head * self.head_dim), self._bf16)
         _launch("gpt_op_kv_append", self.device, self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope),
                 int(qk_norm), rope_base, eps, q.data_ptr())
         return q
@@ -128,26 +128,27 @@ class KVCache:
         """(k, v): bf16 [M, n_kv_head, head_dim], the values cached at the batch's new positions."""
         shape = (M, self.n_kv_head, self.head_dim)
         assert batch.device == self.device, "batch: on another device than the cache"
-        k = _out(k, "k", shape, torch.bfloat16, self.device)
-        v = _out(v, "v", shape, torch.bfloat16, self.device)
+        k = _out(k, "k", shape, self._bf16)
+        v = _out(v, "v", shape, self._bf16)
         _launch("gpt_op_kv_read", self.device, self._ref, batch._ref, M, k.data_ptr(), v.data_ptr())
         return k, v
 
-    def _heads(self, q: torch.Tensor) -> int:
-        assert q.dim() == 2 and q.shape[1] % self.head_dim == 0, "q: [M, n_head head_dim]"
-        return q.shape[1] // self.head_dim
+    def _rows(self, batch: KVBatch, q: torch.Tensor):
+        """Rows and heads of the queries, which are checked."""
+        shape = q.shape
+        assert len(shape) == 2 and shape[1] % self.head_dim == 0, "q: [M, n_head head_dim]"
+        _check(q, "q", torch.bfloat16, self.device)
+        assert batch.device == self.device, "batch: on another device than the cache"
+        return shape[0], shape[1] // self.head_dim
 
     def select(self, batch: KVBatch, q: torch.Tensor, n_select: int, *, n_first: int = 1, n_last: int = 1,
                blocks: torch.Tensor | None = None, scores: torch.Tensor | None = None):
         """(blocks int32 [M, n_kv_head, n_select], scores fp32 [M, n_kv_head, max_blocks]): the blocks each
         new token attends to, by the bound of their keys' scores; the first ``n_first`` and last ``n_last``
         visible ones always."""
-        M, H = q.shape[0], self._heads(q)
-        _check(q, "q", torch.bfloat16, self.device)
-        assert batch.device == self.device, "batch: on another device than the cache"
-        shapes = (M, self.n_kv_head, n_select), (M, self.n_kv_head, batch.block_table.shape[1])
-        blocks = _out(blocks, "blocks", shapes[0], torch.int32, self.device)
-        scores = _out(scores, "scores", shapes[1], torch.float32, self.device)
+        M, H = self._rows(batch, q)
+        blocks = _out(blocks, "blocks", (M, self.n_kv_head, n_select), self._i32)
+        scores = _out(scores, "scores", (M, self.n_kv_head, batch.max_blocks), self._f32)
         _launch("gpt_op_kv_select", self.device, self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
                 blocks.data_ptr(), scores.data_ptr())
         return blocks, scores
@@ -168,16 +169,14 @@ class KVCache:
         over all earlier keys, over the last ``window`` and itself, or over the listed ``blocks`` (of each
         list the first min(length, visible blocks) entries are read: put the visible ones first).
         ``scratch`` (uint8, scratch_bytes) may be passed in; calls that overlap need their own."""
-        M, H = q.shape[0], self._heads(q)
-        _check(q, "q", torch.bfloat16, self.device)
-        assert batch.device == self.device, "batch: on another device than the cache"
+        M, H = self._rows(batch, q)
         n_sel = 0
         if blocks is not None:
             n_sel = blocks.shape[-1]
             _check(blocks, "blocks", torch.int32, self.device, (M, self.n_kv_head, n_sel))
             assert n_sel > 0, "blocks: at least one entry a list"
-        o = torch.empty_like(q) if o is None else _out(o, "o", q.shape, torch.bfloat16, self.device)
-        lse = _out(lse, "lse", (M, H), torch.float32, self.device)
+        o = torch.empty_like(q) if o is None else _out(o, "o", q.shape, self._bf16)
+        lse = _out(lse, "lse", (M, H), self._f32)
         if scratch is None:
             scratch = self.tiles.new_empty(self.scratch_bytes(batch, M, H, n_sel))
         else:
