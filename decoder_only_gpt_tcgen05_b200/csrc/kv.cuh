@@ -144,8 +144,10 @@ __device__ __forceinline__ float bf16_hi(unsigned int u) { return __uint_as_floa
 
 // Host side: checks of the two descriptions every call takes.
 int kv_check(const char* what, const gpt_kv_cache* c, const gpt_kv_batch* b, int M);
+// Most new tokens of a sequence: one each without cu_new, whatever the field holds.
+inline int kv_max_new(const gpt_kv_batch* b) { return b->cu_new ? b->max_new : 1; }
 inline KvRows kv_rows(const gpt_kv_batch* b, int M) {
-  return KvRows{b->block_table, b->lens, b->cu_new, b->n_seq, b->max_blocks, b->max_new, M};
+  return KvRows{b->block_table, b->lens, b->cu_new, b->n_seq, b->max_blocks, kv_max_new(b), M};
 }
 
 // Calls f(KvGeom<bits, hd>()) for the cache's geometry (kv_check has admitted it).

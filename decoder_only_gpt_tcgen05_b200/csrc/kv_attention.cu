@@ -979,7 +979,7 @@ static int attend_plan(const char* what, const gpt_kv_cache* c, const gpt_kv_bat
   const std::string w(what);
   if (H < 1 || H % c->n_kv_head) return set_error(ST_INVALID_ARG, w + ": H must be a multiple of n_kv_head");
   const long long G = H / c->n_kv_head;
-  const long long max_new = b->cu_new ? b->max_new : 1;
+  const long long max_new = kv_max_new(b);
   const long long rows = sparse ? G : max_new * G;  // query rows of a sequence (sparse: of a token) and kv head
   AttendPlan p;
   // Query rows of a tile: 4, 8 or 16 by the rows there are.  Measured at 9 to 16 rows and more (8 bits,
@@ -1095,7 +1095,6 @@ GPT_API int gpt_op_attention_kv(const gpt_kv_cache* cache, const gpt_kv_batch* b
   a.tiles = static_cast<const uint8_t*>(cache->tiles);
   a.sel = sel;
   a.rows = kv_rows(batch, M);
-  if (!batch->cu_new) a.rows.max_new = 1;
   a.n_blocks = cache->n_blocks;
   a.block_bytes = (unsigned int)block_bytes;
   a.H = H;

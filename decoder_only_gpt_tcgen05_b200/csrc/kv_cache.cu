@@ -548,7 +548,7 @@ int kv_check(const char* what, const gpt_kv_cache* c, const gpt_kv_batch* b, int
   if (!c->tiles) return set_error(ST_INVALID_ARG, w + ": null tiles");
   if (misaligned(c->tiles, 16) || misaligned(c->bounds, 16))
     return set_error(ST_INVALID_ARG, w + ": tiles and bounds must be 16-byte aligned");
-  if (b->n_seq < 0 || b->max_blocks < 1 || b->max_new < 0)
+  if (b->n_seq < 0 || b->max_blocks < 1 || kv_max_new(b) < 0)
     return set_error(ST_INVALID_ARG, w + ": n_seq and max_new must be >= 0, max_blocks >= 1");
   if (M < 0) return set_error(ST_INVALID_ARG, w + ": M must be >= 0");
   if (b->max_blocks > (1 << 24)) return set_error(ST_UNSUPPORTED, w + ": max_blocks above 2^24");
@@ -591,11 +591,11 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     return set_error(ST_INVALID_ARG, "kv_append: rope_base must be finite and > 1");
   if (qk_norm && !(eps > 0.f && std::isfinite(eps)))
     return set_error(ST_INVALID_ARG, "kv_append: eps must be finite and > 0");
-  if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
+  const int max_new = kv_max_new(batch);
+  if (M == 0 || batch->n_seq == 0 || max_new == 0) return ST_OK;
   if (!qkv || !q_out) return set_error(ST_INVALID_ARG, "kv_append: null qkv or q_out");
   if (misaligned(qkv, 16) || misaligned(q_out, 16))
     return set_error(ST_INVALID_ARG, "kv_append: qkv and q_out must be 16-byte aligned");
-  const int max_new = batch->cu_new ? batch->max_new : 1;
   const long long bps = ((long long)max_new + kKvBlock - 2) / kKvBlock + 1;  // blocks that max_new tokens can touch
   if (bps * batch->n_seq > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_append: n_seq x max_new too large");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -617,8 +617,7 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
     const int hw = max_new >= 8 ? H + 2 * Hkv : (H + 2 * Hkv + 3) / 4;
     long long y = ctas >= 4LL * num_sms() ? 1 : (4LL * num_sms() + ctas - 1) / ctas;
     if (y > (hw + 7) / 8) y = (hw + 7) / 8;
-    KvRows r = kv_rows(batch, M);
-    r.max_new = max_new;
+    const KvRows r = kv_rows(batch, M);
     constexpr int SMEM = kKvBlock * G::HD * 4 + kAppendThreads / 32 * kAppendRing * 1024;
     static bool attr_set[64] = {};
     int dev = 0;
@@ -639,12 +638,12 @@ GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch,
                            void* stream) {
   set_error(ST_OK, "");
   GPTK_TRY(kv_check("kv_read", cache, batch, M));
-  if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
+  const int max_new = kv_max_new(batch);
+  if (M == 0 || batch->n_seq == 0 || max_new == 0) return ST_OK;
   if (!k_out || !v_out) return set_error(ST_INVALID_ARG, "kv_read: null k_out or v_out");
   if (misaligned(k_out, 16) || misaligned(v_out, 16))
     return set_error(ST_INVALID_ARG, "kv_read: k_out and v_out must be 16-byte aligned");
   const int Hkv = cache->n_kv_head;
-  const int max_new = batch->cu_new ? batch->max_new : 1;
   const long long bps = ((long long)max_new + kKvBlock - 2) / kKvBlock + 1;  // blocks that max_new tokens can touch
   if (bps * batch->n_seq > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_read: n_seq x max_new too large");
   const int groups = (Hkv + 7) / 8, warps = (Hkv + groups - 1) / groups;  // heads spread evenly over the CTAs
@@ -655,8 +654,7 @@ GPT_API int gpt_op_kv_read(const gpt_kv_cache* cache, const gpt_kv_batch* batch,
   Prof prof(PK_MISC, 0, (double)M * Hkv * cache->head_dim * (4 + cache->bits / 4.0), st);
   return kv_dispatch(cache, [&](auto g) -> int {
     using G = decltype(g);
-    KvRows r = kv_rows(batch, M);
-    r.max_new = max_new;
+    const KvRows r = kv_rows(batch, M);
     GPTK_CUDA(launch_pdl(kv_read_kernel<G>, dim3((unsigned)(bps * batch->n_seq), (unsigned)groups), dim3(32 * warps), 0,
                          st, r, (int)bps, static_cast<const uint8_t*>(cache->tiles), (int)cache->n_blocks, Hkv,
                          static_cast<__nv_bfloat16*>(k_out), static_cast<__nv_bfloat16*>(v_out), ctl));

@@ -235,7 +235,7 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   if ((long long)M * Hkv > 0x7fffffffLL) return set_error(ST_UNSUPPORTED, "kv_select: M x n_kv_head too large");
   const long long chunks = ((long long)batch->max_blocks + kScoreChunk - 1) / kScoreChunk;
   if (chunks > 65535) return set_error(ST_UNSUPPORTED, "kv_select: max_blocks above 64 x 65535");
-  if (M == 0 || batch->n_seq == 0 || batch->max_new == 0) return ST_OK;
+  if (M == 0 || batch->n_seq == 0 || kv_max_new(batch) == 0) return ST_OK;
   if (!q || !blocks || !scores) return set_error(ST_INVALID_ARG, "kv_select: null q, blocks or scores");
   if ((reinterpret_cast<uintptr_t>(q) & 15) || (reinterpret_cast<uintptr_t>(blocks) & 3) ||
       (reinterpret_cast<uintptr_t>(scores) & 3))
@@ -243,8 +243,7 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const DevCtl ctl = device_ctl();
   if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
-  KvRows r = kv_rows(batch, M);
-  if (!batch->cu_new) r.max_new = 1;
+  const KvRows r = kv_rows(batch, M);
   const int hd = cache->head_dim;
   {
     Prof prof(PK_MISC, 0, (double)M * Hkv * batch->max_blocks * (4.0 * hd + 4), st);

@@ -852,3 +852,39 @@ def test_binding_refuses_wrong_tensors():
         g.KVCache(4, 2, 64, bits=8, device=DEV, bounds=False).select(batch, q, 2)
     with pytest.raises(g.GptError):
         w.cache.attend(batch, q, scratch=torch.empty(256, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("max_new", [0, -3, 7])
+def test_the_field_max_new_does_not_matter_without_cu_new(max_new):
+    """Through the C calls (the binding always passes 1): append, read, selection and attention of one token
+    a sequence do the same work whatever the field holds."""
+    import ctypes as C
+
+    from decoder_only_gpt_tcgen05_b200._lib import KVBatchParams
+    g = _g()
+    H, hd = 4, 64
+    raw = bf(normal((3, (H + 4) * hd), 6))
+    outs = []
+    for field in (1, max_new):
+        w = World(8, hd, 2, [200, 130, 64], 90)
+        lens, table = i32(w.lens), i32(w.table)
+        b = C.byref(KVBatchParams(table.data_ptr(), lens.data_ptr(), None, 3, w.W, field))
+        c, st = w.cache._ref, torch.cuda.current_stream(DEV).cuda_stream
+        q = torch.full((3, H * hd), 7.0, dtype=torch.bfloat16, device=DEV)
+        k = torch.full((3, 2, hd), 7.0, dtype=torch.bfloat16, device=DEV)
+        v, o = k.clone(), q.clone()
+        blocks = torch.full((3, 2, 3), 77, dtype=torch.int32, device=DEV)
+        scores, lse = torch.full((3, 2, w.W), 7.0, device=DEV), torch.full((3, H), 7.0, device=DEV)
+        n = C.c_size_t()
+        g._lib.call("gpt_op_kv_append", c, b, raw.data_ptr(), 3, H, 1, 1, 1e4, 1e-5, q.data_ptr(), st)
+        g._lib.call("gpt_op_kv_read", c, b, 3, k.data_ptr(), v.data_ptr(), st)
+        g._lib.call("gpt_op_kv_select", c, b, q.data_ptr(), 3, H, 3, 1, 1, blocks.data_ptr(), scores.data_ptr(), st)
+        g._lib.call("gpt_op_attention_kv_scratch_size", c, b, 3, H, 0, C.byref(n))
+        scratch = torch.empty(n.value, dtype=torch.uint8, device=DEV)
+        g._lib.call("gpt_op_attention_kv", c, b, q.data_ptr(), 3, H, -1, None, 0, o.data_ptr(), lse.data_ptr(),
+                    scratch.data_ptr(), n.value, st)
+        g.model.sync_status(DEV)
+        outs.append((q, k, v, o, blocks, scores, lse, w.cache.tiles))
+        assert not any(torch.all(t == 7) or torch.all(t == 77) for t in outs[-1])
+    for x, y in zip(*outs):
+        assert torch.equal(x, y)

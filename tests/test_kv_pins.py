@@ -170,3 +170,20 @@ def test_nothing_to_do_is_no_error_and_launches_nothing():
         assert L.gpt_op_kv_select(c, b, P, M, 4, 4, 1, 1, P, P, None) == 0
         assert L.gpt_op_attention_kv(c, b, P, M, 4, -1, None, 0, P, P, P, 1 << 40, None) == 0
     assert g.ops.launch_count() == before
+
+
+@pytest.mark.parametrize("max_new", [0, -3, 7])
+def test_without_cu_new_the_field_max_new_is_ignored(max_new):
+    """Every sequence has one new token then, so there is work and missing tensors are refused; the
+    attention's scratch is that of one token each."""
+    import decoder_only_gpt_tcgen05_b200 as g
+    L = g.lib()
+    c, b = _args(batch=dict(cu_new=None, max_new=max_new))
+    assert L.gpt_op_kv_append(c, b, None, 8, 4, 1, 1, 1e4, 1e-5, P, None) == 1
+    assert L.gpt_op_kv_read(c, b, 8, None, P, None) == 1
+    assert L.gpt_op_kv_select(c, b, None, 8, 4, 4, 1, 1, P, P, None) == 1
+    assert L.gpt_op_attention_kv(c, b, None, 8, 4, -1, None, 0, P, P, P, 1 << 40, None) == 1
+    n, one = C.c_size_t(), C.c_size_t()
+    assert L.gpt_op_attention_kv_scratch_size(c, b, 8, 4, 0, C.byref(n)) == 0
+    assert L.gpt_op_attention_kv_scratch_size(c, _args(batch=dict(cu_new=None, max_new=1))[1], 8, 4, 0, C.byref(one)) == 0
+    assert n.value == one.value
