@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   constexpr int TL = NT == 2 ? (G::BITS == 8 && HD == 128 ? 2 : 1) : QC == 2 ? 2 : U / 16;  // 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ uint64_t bars[C::WARPS][C::STAGES];
-  __shared__ int meta[C::WARPS][C::STAGES];
+  __shared__ int meta[C::WARPS][C::STAGES];  // of a stage's unit: first key; -1: none; -2 - first key: bad block
   __shared__ long long s_pre[kScanSmem + 1];
   __shared__ int s_cnt[kScanSmem + 1];
   __shared__ long long s_warp[C::WARPS];
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
     if (lane == 0) {
       const uint32_t bar = bar0 + 8 * stage;
       const bool ok = (unsigned int)f_phys < (unsigned int)p.n_blocks;
-      meta[warp][stage] = f_kb < 0 ? -1 : ok ? f_kb : -2;
+      meta[warp][stage] = f_kb < 0 ? -1 : ok ? f_kb : -2 - f_kb;
       if (f_kb >= 0 && ok) {
         const uint8_t* src = p.tiles + (unsigned long long)f_phys * p.block_bytes +
                              (unsigned int)(fh * G::TILE + (U == 64 ? 0 : f_kb / kKvRec % 2 * G::REC));
@@ -808,11 +808,15 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         }
       }
     }
-    if (kb0 == -2) {  // a block number out of range: the rows become NaN
+    if (kb0 < -1) {  // a block number out of range: the rows that see one of the unit's keys become NaN
+      const int kb = -2 - kb0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int q = 0; q < QC; ++q) l[nt][q] = __uint_as_float(0x7fc00000u);
+        for (int q = 0; q < QC; ++q) {
+          const int pos = s_pos[warp][QC == 1 ? c : nt * 8 + 2 * c + q];
+          if (kb <= pos && (window < 0 || kb + U - 1 >= pos - window)) l[nt][q] = __uint_as_float(0x7fc00000u);
+        }
     }
     __syncwarp();
     fetch(u + C::STAGES);

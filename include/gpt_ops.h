@@ -231,7 +231,8 @@ typedef struct gpt_kv_cache {
  * lens[b] <= 64 max_blocks and rows within [0, M); one that has not is left
  * out of the call.  cu_new must not decrease; a row that two sequences claim
  * holds the result of either.  A block number outside [0, n_blocks) that a call would use
- * is never followed: append skips those tokens, read and attention give NaN.
+ * is never followed: append skips those tokens, read gives them as NaN, and
+ * attention the rows that see a key of that block.
  * Both are reported by gpt_sync_status (GPT_ERR_INVALID_ARG). */
 typedef struct gpt_kv_batch {
   const int32_t* block_table;  /* [n_seq, max_blocks] cache block of each 64 tokens, in order        */

@@ -888,3 +888,62 @@ def test_the_field_max_new_does_not_matter_without_cu_new(max_new):
         assert not any(torch.all(t == 7) or torch.all(t == 77) for t in outs[-1])
     for x, y in zip(*outs):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("bits,hd,H,Hkv,new,window", [
+    (8, 128, 2, 2, 4, -1), (4, 128, 4, 2, 6, -1), (8, 64, 8, 1, 5, -1), (4, 64, 1, 1, 3, -1),   # tiles of 4, 8 and 16
+    (8, 128, 2, 2, 4, 0), (8, 128, 4, 1, 4, 70), (4, 128, 2, 2, 40, 20), (4, 64, 2, 1, 66, 64), (8, 64, 6, 2, 70, 31)])
+def test_a_bad_block_number_shows_in_the_rows_that_see_its_keys(bits, hd, H, Hkv, new, window):
+    """New tokens before, in and behind a block whose number is bad: NaN exactly in the rows of which a key
+    lies in it, by causality and by the window."""
+    g = _g()
+    for first in (64 - new // 2, 128 - new // 2, 128, 192 - new // 2, 150):     # position of the first new token
+        w = World(bits, hd, Hkv, [first + new], 91)
+        q = bf(normal((new, H * hd), 4))
+        for j in range((first + new - 1) // 64 + 1):
+            table = w.table.copy()
+            table[0, j] = w.n_blocks + 5
+            o, lse = w.cache.attend(g.KVBatch(i32(table), i32(w.lens), i32([0, new]), max_new=new), q, window=window)
+            p = np.arange(first, first + new)
+            sees = (p >= 64 * j) & ((p - window <= 64 * j + 63) if window >= 0 else True)
+            if sees.any():
+                with pytest.raises(g.GptError):
+                    g.model.sync_status(DEV)
+            else:
+                g.model.sync_status(DEV)
+            on, ln = np.isnan(f64(o)), np.isnan(f64(lse))
+            assert np.array_equal(on.all(1), sees) and np.array_equal(on.any(1), sees), (first, j)
+            assert np.array_equal(ln.all(1), sees) and np.array_equal(ln.any(1), sees), (first, j)
+            if not sees.all():
+                part = np.flatnonzero(~sees)
+                ref = w.cache.attend(w.batch([new])[0], q, window=window)
+                for m in part:
+                    n = first + m + 1
+                    ro, rl, av = O.kv.attend(f64(q)[m].reshape(H, hd), w.k[0][:n], w.v[0][:n],
+                                             np.repeat((np.arange(n) >= n - 1 - window if window >= 0 else np.ones(n))
+                                                       [None].astype(float), Hkv, 0))
+                    wt = np.zeros((Hkv, first + new))
+                    wt[:, :n] = 1.0
+                    to, tl = attend_bounds(w, 0, f64(q)[m].reshape(H, hd), ro, rl, av, wt)
+                    assert np.all(np.abs(f64(o)[m].reshape(H, hd) - ro) <= to) and np.all(np.abs(f64(lse)[m] - rl) <= tl)
+                assert np.all(np.isfinite(f64(ref[0])))
+
+
+def test_a_bad_block_number_in_a_list_shows_in_its_row_only():
+    g = _g()
+    w = World(8, 128, 2, [140, 70], 92)
+    table = w.table.copy()
+    table[0, 1] = -9
+    batch = g.KVBatch(i32(table), i32(w.lens), i32([0, 14, 16]), max_new=14)
+    q = bf(normal((16, 256), 4))
+    sel = np.zeros((16, 2, 2), int)
+    sel[:, :, 1] = -1
+    sel[3, 0], sel[5, 1] = [0, 1], [1, 0]         # positions 129 and 131 see block 1
+    sel[9, 0] = [2, 0]
+    o, lse = w.cache.attend(batch, q, blocks=i32(sel))
+    with pytest.raises(g.GptError):
+        g.model.sync_status(DEV)
+    bad = np.zeros((16, 2), bool)
+    bad[3, 0] = bad[5, 1] = True
+    assert np.array_equal(np.isnan(f64(o).reshape(16, 2, 128)).all(-1), bad) and np.array_equal(np.isnan(f64(lse)), bad)
+    assert np.array_equal(np.isnan(f64(o).reshape(16, 2, 128)).any(-1), bad)
