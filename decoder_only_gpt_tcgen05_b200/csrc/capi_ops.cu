@@ -11,17 +11,31 @@ using namespace gptk;
 
 namespace gptk {
 // Waits on an mbarrier that nothing arrives at, through the same bounded wait as every
-// pipeline kernel: after ctl.timeout_ns it records DEV_ERR_TIMEOUT and returns.
+// pipeline kernel: after ctl.timeout_ns it records DEV_ERR_TIMEOUT (site 99) and returns.  Before that, the
+// wait for copies in flight: the abort flag is up and a second warp arrives after a quarter of the limit,
+// which the wait must have seen (site 98 otherwise).
 __global__ void wait_probe_kernel(DevCtl ctl) {
-  __shared__ uint64_t bar;
+  __shared__ uint64_t bar, late;
   __shared__ int abort_flag;
   if (threadIdx.x == 0) {
     mbar_init(&bar, 1);
-    abort_flag = 0;
+    mbar_init(&late, 1);
+    abort_flag = 1;
     fence_mbar_init();
   }
   __syncthreads();
-  if (threadIdx.x == 0) mbar_wait(&bar, 0, ctl, &abort_flag, 99);
+  const uint64_t t0 = globaltimer();
+  if (threadIdx.x == 32) {
+    while (globaltimer() - t0 < ctl.timeout_ns / 4) {
+    }
+    mbar_arrive(&late);
+  }
+  if (threadIdx.x == 0 && !mbar_drain(&late, 0, ctl, t0)) dev_report(ctl, DEV_ERR_TIMEOUT, 98);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    mbar_wait(&bar, 0, ctl, &abort_flag, 99);
+  }
 }
 
 // The attention forward's two exponentials, element pairs (x[2i], x[2i+1]) -> out
@@ -43,7 +57,7 @@ GPT_API int gpt_op_wait_probe(unsigned long long timeout_ns, void* stream) {
   if (!ctl.status) return set_error(ST_CUDA, "device status word unavailable");
   ctl.timeout_ns = timeout_ns;
   Prof prof(PK_MISC, 0, 0, static_cast<cudaStream_t>(stream));
-  wait_probe_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(ctl);
+  wait_probe_kernel<<<1, 64, 0, static_cast<cudaStream_t>(stream)>>>(ctl);
   GPTK_CUDA(cudaGetLastError());
   return ST_OK;
 }

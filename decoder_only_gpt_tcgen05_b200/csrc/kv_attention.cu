@@ -563,9 +563,10 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   for (int u = 0; u < units; ++u) {
     const int stage = u % C::STAGES;
     if (!mbar_wait(&bars[warp][stage], u / C::STAGES & 1, p.ctl, &abort_flag, 20)) {
-      // give up: the copies still in flight land in this CTA's shared memory, so wait for them too
-      for (int i = u + 1; i < u + C::STAGES && i < units; ++i)
-        mbar_wait(&bars[warp][i % C::STAGES], i / C::STAGES & 1, p.ctl, &abort_flag, 21);
+      // give up: the copies of units u .. u + STAGES - 1 may still be in flight into this CTA's shared memory
+      const uint64_t t0 = globaltimer();
+      for (int i = u; i < u + C::STAGES && i < units; ++i)
+        mbar_drain(&bars[warp][i % C::STAGES], i / C::STAGES & 1, p.ctl, t0);
       return;
     }
     const int kb0 = meta[warp][stage];

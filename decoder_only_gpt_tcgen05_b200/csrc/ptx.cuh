@@ -102,6 +102,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, const 
   }
 }
 
+// Waits, on the way out of a kernel that has given up, until the phase has completed: a copy in flight must
+// not land in shared memory that is another CTA's by then.  Goes by its own limit, ctl.timeout_ns from t0 on
+// (one limit for all the barriers of a warp), whatever the CTA's abort flag says; false when that has passed.
+__device__ __forceinline__ bool mbar_drain(uint64_t* bar, uint32_t parity, const DevCtl& ctl, uint64_t t0) {
+  while (!mbar_try_wait(bar, parity))
+    if (globaltimer() - t0 > ctl.timeout_ns) return false;
+  return true;
+}
+
 // ----------------------------------------------------------------- TMA
 
 __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {

@@ -144,8 +144,10 @@ GPT_API int gpt_op_lmhead_ce_fwd_noalloc(const void* x, const void* w, const int
  * that waits on an mbarrier nothing ever arrives at, through the same bounded
  * wait every pipeline kernel uses.  After timeout_ns (at most 10 s) the kernel
  * records a timeout in the device status word and returns, so the next
- * gpt_sync_status() reports GPT_ERR_DEVICE_TIMEOUT and the context stays
- * usable.  Nothing faults, traps or hangs. */
+ * gpt_sync_status() reports GPT_ERR_DEVICE_TIMEOUT (site 99) and the context
+ * stays usable.  Before that it waits as a kernel that gives up does for its
+ * copies in flight, on an mbarrier that is arrived at after timeout_ns / 4
+ * (site 98 if that wait ended early).  Nothing faults, traps or hangs. */
 GPT_API int gpt_op_wait_probe(unsigned long long timeout_ns, void* stream);
 
 /* The attention softmax's exponential and an FMA-pipe alternative to it, for

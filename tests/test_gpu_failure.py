@@ -44,3 +44,15 @@ def test_out_of_range_token_is_reported():
         g.model.sync_status(DEV)
     assert e.value.code == 1 and "token id" in str(e.value)
     g.model.sync_status(DEV)
+
+
+def test_a_kernel_that_gives_up_still_waits_for_its_copies():
+    """The probe drains a barrier that completes late, with the abort flag up, before the wait that runs out."""
+    import decoder_only_gpt_tcgen05_b200 as g
+    from decoder_only_gpt_tcgen05_b200._lib import GptError
+    g.model.sync_status(DEV)
+    g._lib.call("gpt_op_wait_probe", 20_000_000, torch.cuda.current_stream(DEV).cuda_stream)
+    with pytest.raises(GptError) as e:
+        g.model.sync_status(DEV)
+    assert e.value.code == 5 and "site 99," in str(e.value)
+    g.model.sync_status(DEV)
