@@ -8,6 +8,7 @@ the host, so a step can be captured into a CUDA graph and replayed with new cont
 from __future__ import annotations
 
 import ctypes as C
+import operator
 
 import torch
 
@@ -59,11 +60,23 @@ def _out(t, name: str, shape, like: torch.Tensor) -> torch.Tensor:
     return t
 
 
+def _frozen(*names):
+    """Read-only attributes ``name``, held as ``_name``: the library's calls go by the pointers and sizes of
+    the constructor, so an assignment would change nothing but let go of memory that they still use."""
+    def deco(cls):
+        for n in names:
+            setattr(cls, n, property(operator.attrgetter("_" + n)))
+        return cls
+    return deco
+
+
+@_frozen("block_table", "lens", "cu_new", "max_new", "device", "n_seq", "max_blocks")
 class KVBatch:
     """Sequences and their new tokens (gpt_kv_batch): ``block_table`` int32 [n_seq, max_blocks], ``lens``
     int32 [n_seq] (new tokens included) and ``cu_new`` int32 [n_seq + 1], the first row of each
     sequence in the row tensors (None: one new token each, row b for sequence b); ``max_new``: the most
-    new tokens a sequence has.  The tensors are kept, not copied: update them in place between steps."""
+    new tokens a sequence has.  The tensors are kept, not copied: update them in place between steps
+    (``batch.lens.add_(1)``, ``batch.lens.copy_(...)``); the attributes cannot be assigned to."""
 
     def __init__(self, block_table: torch.Tensor, lens: torch.Tensor, cu_new: torch.Tensor | None = None, *,
                  max_new: int = 1):
@@ -75,17 +88,19 @@ class KVBatch:
         if cu_new is not None:
             _check(cu_new, "cu_new", torch.int32, dev, (n + 1,))
         assert max_new >= 0 and (cu_new is not None or max_new == 1), "max_new: without cu_new it is 1"
-        self.block_table, self.lens, self.cu_new, self.max_new, self.device = block_table, lens, cu_new, max_new, dev
-        self.n_seq, self.max_blocks = n, w
+        self._block_table, self._lens, self._cu_new, self._max_new, self._device = block_table, lens, cu_new, max_new, dev
+        self._n_seq, self._max_blocks = n, w
         self._c = KVBatchParams(block_table.data_ptr(), lens.data_ptr(), cu_new.data_ptr() if cu_new is not None else None,
                                 n, w, max_new)
         self._ref = C.byref(self._c)
 
 
+@_frozen("n_blocks", "n_kv_head", "head_dim", "bits", "tiles", "bounds", "device")
 class KVCache:
     """The cache of one attention layer: ``n_blocks`` blocks of 64 tokens for ``n_kv_head`` heads of
     ``head_dim`` (64 or 128) in ``bits`` (4 or 8).  ``bounds``: keep the elementwise key bounds of each
-    block that ``select`` needs.  ``tiles`` and ``bounds`` may be given as tensors made earlier."""
+    block that ``select`` needs.  ``tiles`` and ``bounds`` may be given as tensors made earlier; like the
+    sizes they cannot be assigned to later, their contents can."""
 
     def __init__(self, n_blocks: int, n_kv_head: int, head_dim: int, *, bits: int = 8, device="cuda:0",
                  tiles: torch.Tensor | None = None, bounds: torch.Tensor | bool = True):
@@ -102,8 +117,8 @@ class KVCache:
             bounds = None
         if bounds is not None:
             _check(bounds, "bounds", torch.bfloat16, dev, (n_blocks, n_kv_head, 2, head_dim))
-        self.n_blocks, self.n_kv_head, self.head_dim, self.bits = n_blocks, n_kv_head, head_dim, bits
-        self.tiles, self.bounds, self.device = tiles, bounds, dev
+        self._n_blocks, self._n_kv_head, self._head_dim, self._bits = n_blocks, n_kv_head, head_dim, bits
+        self._tiles, self._bounds, self._device = tiles, bounds, dev
         self._scratch = {}
         # what outputs are made like: a new tensor of the same type takes less time than one by type and device
         self._bf16, self._f32, self._i32 = (torch.empty(0, dtype=t, device=dev)
@@ -117,29 +132,29 @@ class KVCache:
         """Writes the new tokens' keys and values (``qkv``: bf16 [M, (n_head + 2 n_kv_head) head_dim], raw)
         and returns their queries after RoPE and QK-norm, bf16 [M, n_head head_dim]."""
         M = qkv.shape[0]
-        _check(qkv, "qkv", torch.bfloat16, self.device, (M, (n_head + 2 * self.n_kv_head) * self.head_dim))
-        assert batch.device == self.device, "batch: on another device than the cache"
-        q = _out(q, "q", (M, n_head * self.head_dim), self._bf16)
-        _launch("gpt_op_kv_append", self.device, self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope),
+        _check(qkv, "qkv", torch.bfloat16, self._device, (M, (n_head + 2 * self._n_kv_head) * self._head_dim))
+        assert batch._device == self._device, "batch: on another device than the cache"
+        q = _out(q, "q", (M, n_head * self._head_dim), self._bf16)
+        _launch("gpt_op_kv_append", self._device, self._ref, batch._ref, qkv.data_ptr(), M, n_head, int(rope),
                 int(qk_norm), rope_base, eps, q.data_ptr())
         return q
 
     def read(self, batch: KVBatch, M: int, *, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
         """(k, v): bf16 [M, n_kv_head, head_dim], the values cached at the batch's new positions."""
-        shape = (M, self.n_kv_head, self.head_dim)
-        assert batch.device == self.device, "batch: on another device than the cache"
+        shape = (M, self._n_kv_head, self._head_dim)
+        assert batch._device == self._device, "batch: on another device than the cache"
         k = _out(k, "k", shape, self._bf16)
         v = _out(v, "v", shape, self._bf16)
-        _launch("gpt_op_kv_read", self.device, self._ref, batch._ref, M, k.data_ptr(), v.data_ptr())
+        _launch("gpt_op_kv_read", self._device, self._ref, batch._ref, M, k.data_ptr(), v.data_ptr())
         return k, v
 
     def _rows(self, batch: KVBatch, q: torch.Tensor):
         """Rows and heads of the queries, which are checked."""
         shape = q.shape
-        assert len(shape) == 2 and shape[1] % self.head_dim == 0, "q: [M, n_head head_dim]"
-        _check(q, "q", torch.bfloat16, self.device)
-        assert batch.device == self.device, "batch: on another device than the cache"
-        return shape[0], shape[1] // self.head_dim
+        assert len(shape) == 2 and shape[1] % self._head_dim == 0, "q: [M, n_head head_dim]"
+        _check(q, "q", torch.bfloat16, self._device)
+        assert batch._device == self._device, "batch: on another device than the cache"
+        return shape[0], shape[1] // self._head_dim
 
     def select(self, batch: KVBatch, q: torch.Tensor, n_select: int, *, n_first: int = 1, n_last: int = 1,
                blocks: torch.Tensor | None = None, scores: torch.Tensor | None = None):
@@ -147,15 +162,15 @@ class KVCache:
         new token attends to, by the bound of their keys' scores; the first ``n_first`` and last ``n_last``
         visible ones always."""
         M, H = self._rows(batch, q)
-        blocks = _out(blocks, "blocks", (M, self.n_kv_head, n_select), self._i32)
-        scores = _out(scores, "scores", (M, self.n_kv_head, batch.max_blocks), self._f32)
-        _launch("gpt_op_kv_select", self.device, self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
+        blocks = _out(blocks, "blocks", (M, self._n_kv_head, n_select), self._i32)
+        scores = _out(scores, "scores", (M, self._n_kv_head, batch._max_blocks), self._f32)
+        _launch("gpt_op_kv_select", self._device, self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
                 blocks.data_ptr(), scores.data_ptr())
         return blocks, scores
 
     def scratch_bytes(self, batch: KVBatch, M: int, n_head: int, n_sel: int = 0) -> int:
         """Bytes of scratch that attend needs; it goes by the sizes alone, so it is asked for once a size."""
-        key = (batch.n_seq, batch.max_new, batch.cu_new is None, M, n_head, n_sel > 0)
+        key = (batch._n_seq, batch._max_new, batch._cu_new is None, M, n_head, n_sel > 0)
         n = self._scratch.get(key)
         if n is None:
             out = C.c_size_t()
@@ -173,15 +188,15 @@ class KVCache:
         n_sel = 0
         if blocks is not None:
             n_sel = blocks.shape[-1]
-            _check(blocks, "blocks", torch.int32, self.device, (M, self.n_kv_head, n_sel))
+            _check(blocks, "blocks", torch.int32, self._device, (M, self._n_kv_head, n_sel))
             assert n_sel > 0, "blocks: at least one entry a list"
         o = torch.empty_like(q) if o is None else _out(o, "o", q.shape, self._bf16)
         lse = _out(lse, "lse", (M, H), self._f32)
         if scratch is None:
-            scratch = self.tiles.new_empty(self.scratch_bytes(batch, M, H, n_sel))
+            scratch = self._tiles.new_empty(self.scratch_bytes(batch, M, H, n_sel))
         else:
-            _check(scratch, "scratch", torch.uint8, self.device)
-        _launch("gpt_op_attention_kv", self.device, self._ref, batch._ref, q.data_ptr(), M, H, int(window),
+            _check(scratch, "scratch", torch.uint8, self._device)
+        _launch("gpt_op_attention_kv", self._device, self._ref, batch._ref, q.data_ptr(), M, H, int(window),
                 blocks.data_ptr() if blocks is not None else None, n_sel, o.data_ptr(), lse.data_ptr(),
                 scratch.data_ptr(), scratch.numel())
         return o, lse

@@ -187,3 +187,29 @@ def test_without_cu_new_the_field_max_new_is_ignored(max_new):
     assert L.gpt_op_attention_kv_scratch_size(c, b, 8, 4, 0, C.byref(n)) == 0
     assert L.gpt_op_attention_kv_scratch_size(c, _args(batch=dict(cu_new=None, max_new=1))[1], 8, 4, 0, C.byref(one)) == 0
     assert n.value == one.value
+
+
+def test_the_attributes_that_the_calls_go_by_cannot_be_assigned_to():
+    """A batch or cache whose tensor was replaced would go on using the old memory: that is refused, while the
+    tensors' contents may change and every attribute reads as it was given."""
+    import torch
+
+    import decoder_only_gpt_tcgen05_b200 as g
+    table, lens, cu = (torch.arange(n, dtype=torch.int32) for n in (6, 2, 3))
+    b = g.KVBatch(table.view(2, 3), lens, cu, max_new=4)
+    tiles = torch.zeros((5, 2, g.kv.tile_bytes(8, 64)), dtype=torch.uint8)
+    c = g.KVCache(5, 2, 64, bits=8, tiles=tiles)
+    want = {b: dict(lens=lens, cu_new=cu, max_new=4, n_seq=2, max_blocks=3, device=lens.device),
+            c: dict(tiles=tiles, n_blocks=5, n_kv_head=2, head_dim=64, bits=8, device=tiles.device)}
+    for x, attrs in want.items():
+        for name, value in attrs.items():
+            assert getattr(x, name) is value or getattr(x, name) == value
+            with pytest.raises(AttributeError):
+                setattr(x, name, value)
+    for x, name in ((b, "block_table"), (c, "bounds")):
+        assert torch.is_tensor(getattr(x, name))
+        with pytest.raises(AttributeError):
+            setattr(x, name, None)
+    b.lens.add_(1)
+    assert lens.tolist() == [1, 2]
+    assert g.KVBatch(b.block_table, b.lens).cu_new is None and g.KVCache(5, 2, 64, tiles=tiles, bounds=False).bounds is None
