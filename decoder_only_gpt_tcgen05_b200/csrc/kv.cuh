@@ -95,26 +95,28 @@ __device__ __forceinline__ void kv_report_bad(const KvRows& r, const DevCtl& ctl
 }
 
 // The sequence that row m belongs to and the row's position, by a whole block at once (one round of
-// loads): into `at`; b = -1 for a row of no sequence, pos = -1 for one of a sequence out of range.
-// Ends with a barrier.
+// loads), which must have no other barrier under way; b = -1 for a row of no sequence, or of one out of
+// range.  Both numbers are one 64-bit word, so that a row that two sequences claim gets one sequence's.
 struct KvRow {
   int b, pos;
 };
-__device__ __forceinline__ void kv_find_row(const KvRows& r, int m, KvRow* at) {
-  if (threadIdx.x == 0) at->b = -1;
+__device__ __forceinline__ KvRow kv_find_row(const KvRows& r, int m) {
+  __shared__ unsigned long long at;
+  if (threadIdx.x == 0) at = ~0ULL;
   __syncthreads();
+  auto claim = [&](int b) {
+    const KvSeq s = kv_seq(r, b);  // (the loads of several do not wait for one another)
+    const unsigned int i = (unsigned int)m - (unsigned int)s.row0;
+    if (i < (unsigned int)s.n) at = (unsigned long long)(s.len - s.n + i) << 32 | (unsigned int)b;
+  };
   if (!r.cu) {
-    if (threadIdx.x == 0 && m < r.B) {
-      const KvSeq s = kv_seq(r, m);
-      *at = KvRow{m, s.ok ? s.len - 1 : -1};
-    }
+    if (threadIdx.x == 0 && m < r.B) claim(m);
   } else {
-    for (int b = threadIdx.x; b < r.B; b += blockDim.x) {
-      const KvSeq s = kv_seq(r, b);  // (its loads do not wait for one another)
-      if (s.row0 <= m && m < r.cu[b + 1]) *at = KvRow{b, s.ok ? s.len - s.n + (m - s.row0) : -1};
-    }
+    for (int b = threadIdx.x; b < r.B; b += blockDim.x) claim(b);
   }
   __syncthreads();
+  const unsigned long long v = at;
+  return KvRow{(int)(unsigned int)v, (int)(v >> 32)};
 }
 
 // Announces `bytes` (a multiple of 16) on the mbarrier at shared address bar and copies them from

@@ -33,7 +33,6 @@ kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds
   constexpr int NC = HD / 64;
   extern __shared__ double s_q[];  // [G][NC][8 dims of a piece][8 lanes]
   __shared__ int s_phys[kScoreChunk];
-  __shared__ KvRow at;
   pdl_wait();  // (no early trigger: the next kernel's shared memory would leave these loads next to no L1)
   if (blockIdx.x == 0 && blockIdx.y == 0) kv_report_bad(rows, ctl, 5);
   const int m = blockIdx.x / Hkv, h = blockIdx.x - m * Hkv;
@@ -42,10 +41,9 @@ kv_score_kernel(const __nv_bfloat16* q, KvRows rows, const __nv_bfloat16* bounds
     const float v = __bfloat162float(q[((long long)m * Hkv + h) * G * HD + x]);
     s_q[((g * NC + d / 64) * 8 + d % 8) * 8 + (d / 8) % 8] = (double)v;
   }
-  kv_find_row(rows, m, &at);
-  const KvRow row = at;
+  const KvRow row = kv_find_row(rows, m);
   if (row.b < 0) return;
-  const int nb = row.pos < 0 ? 0 : row.pos / kKvBlock + 1;
+  const int nb = row.pos / kKvBlock + 1;
   const int j0 = blockIdx.y * kScoreChunk, j1 = min(j0 + kScoreChunk, rows.W);
   float* out = scores + ((long long)m * Hkv + h) * rows.W;
   if (j0 >= nb) {
@@ -137,16 +135,15 @@ kv_pick_kernel(const float* scores, KvRows rows, int Hkv, int n, int n_first, in
                int* blocks) {
   __shared__ int hist[256];
   __shared__ unsigned int s_key[kPickKeys];
-  __shared__ KvRow at;
   __shared__ int s_bin, s_left;
   __shared__ int wsum[kPickThreads / 32];
   pdl_wait();
   pdl_trigger();
   const int m = blockIdx.x / Hkv;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  kv_find_row(rows, m, &at);
-  if (at.b < 0) return;
-  const int nb = at.pos < 0 ? 0 : at.pos / kKvBlock + 1;
+  const KvRow row = kv_find_row(rows, m);
+  if (row.b < 0) return;
+  const int nb = row.pos / kKvBlock + 1;
   const float* sc = scores + (long long)blockIdx.x * rows.W;
   int* out = blocks + (long long)blockIdx.x * n;
   if (nb <= n) {

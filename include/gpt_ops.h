@@ -231,8 +231,9 @@ typedef struct gpt_kv_cache {
  *
  * A sequence must have 0 <= new tokens <= max_new, lens[b] >= its new tokens,
  * lens[b] <= 64 max_blocks and rows within [0, M); one that has not is left
- * out of the call.  cu_new must not decrease; a row that two sequences claim
- * holds the result of either.  A block number outside [0, n_blocks) that a call would use
+ * out of the call: its rows are left as they are.  cu_new must not decrease;
+ * what a row that two sequences claim holds is not defined (parts of it may be
+ * of the one, parts of the other).  A block number outside [0, n_blocks) that a call would use
  * is never followed: append skips those tokens, read gives them as NaN, and
  * attention the rows that see a key of that block.
  * Both are reported by gpt_sync_status (GPT_ERR_INVALID_ARG). */

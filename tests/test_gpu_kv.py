@@ -947,3 +947,31 @@ def test_a_bad_block_number_in_a_list_shows_in_its_row_only():
     bad[3, 0] = bad[5, 1] = True
     assert np.array_equal(np.isnan(f64(o).reshape(16, 2, 128)).all(-1), bad) and np.array_equal(np.isnan(f64(lse)), bad)
     assert np.array_equal(np.isnan(f64(o).reshape(16, 2, 128)).any(-1), bad)
+
+
+@pytest.mark.parametrize("lens,cu,max_new", [
+    ([200, 10 ** 6, 64], [0, 1, 4, 5], 3),        # longer than its block table
+    ([200, -5, 64], [0, 1, 2, 3], 1),
+    ([200, 130, 64], [0, 1, 9, 10], 1),           # more new tokens than max_new
+    ([200, 2, 64], [0, 1, 5, 6], 4),              # more new tokens than tokens
+    ([200, 130, 64], [0, 1, 2 ** 31 - 1, -2 ** 31], 1),
+    ([200, 0, 64], None, 1),                      # no cu_new: one new token, but no tokens
+])
+def test_selection_leaves_the_rows_of_a_broken_sequence_as_they_are(lens, cu, max_new):
+    w = World(8, 64, 2, [200, 130, 64], 62)
+    g = _g()
+    q = bf(normal((12, 256), 4))
+    blocks = torch.full((12, 2, 3), 77, dtype=torch.int32, device=DEV)
+    scores = torch.full((12, 2, w.W), 77.0, device=DEV)
+    batch = g.KVBatch(i32(w.table), i32(lens), None if cu is None else i32(cu), max_new=max_new)
+    w.cache.select(batch, q, 3, blocks=blocks, scores=scores)
+    with pytest.raises(g.GptError) as e:
+        g.model.sync_status(DEV)
+    assert e.value.code == 1
+    cu = [0, 1, 2, 3] if cu is None else cu
+    good = [0] + ([cu[2]] if 0 <= cu[2] < 12 and cu[3] == cu[2] + 1 else [])
+    rest = [m for m in range(12) if m not in good]
+    assert torch.all(blocks[rest] == 77) and torch.all(scores[rest] == 77.0)
+    assert blocks[0, :, 0].tolist() == [0, 0] and blocks[0, :, 2].tolist() == [3, 3] and not torch.any(scores[0] == 77.0)
+    for m in good[1:]:
+        assert blocks[m].tolist() == [[0, -1, -1]] * 2 and torch.all(scores[m, :, 1:] == -float("inf"))
