@@ -15,6 +15,7 @@ import torch
 from ._lib import KVBatchParams, KVCacheParams, call, check, lib
 
 KV_BLOCK = 64  # tokens of a cache block
+_INT_MAX = 2 ** 31 - 1  # (ctypes cuts a longer number off without a word)
 
 
 def tile_bytes(bits: int, head_dim: int) -> int:
@@ -87,7 +88,8 @@ class KVBatch:
         _check(lens, "lens", torch.int32, dev, (n,))
         if cu_new is not None:
             _check(cu_new, "cu_new", torch.int32, dev, (n + 1,))
-        assert max_new >= 0 and (cu_new is not None or max_new == 1), "max_new: without cu_new it is 1"
+        assert 0 <= max_new <= _INT_MAX, "max_new: 32 bits, not negative"
+        assert cu_new is not None or max_new == 1, "max_new: without cu_new it is 1"
         self._block_table, self._lens, self._cu_new, self._max_new, self._device = block_table, lens, cu_new, max_new, dev
         self._n_seq, self._max_blocks = n, w
         self._c = KVBatchParams(block_table.data_ptr(), lens.data_ptr(), cu_new.data_ptr() if cu_new is not None else None,
@@ -162,6 +164,7 @@ class KVCache:
         new token attends to, by the bound of their keys' scores; the first ``n_first`` and last ``n_last``
         visible ones always."""
         M, H = self._rows(batch, q)
+        assert max(abs(n_select), abs(n_first), abs(n_last)) <= _INT_MAX, "n_select, n_first, n_last: 32 bits"
         blocks = _out(blocks, "blocks", (M, self._n_kv_head, n_select), self._i32)
         scores = _out(scores, "scores", (M, self._n_kv_head, batch._max_blocks), self._f32)
         _launch("gpt_op_kv_select", self._device, self._ref, batch._ref, q.data_ptr(), M, H, n_select, n_first, n_last,
@@ -185,6 +188,7 @@ class KVCache:
         list the first min(length, visible blocks) entries are read: put the visible ones first).
         ``scratch`` (uint8, scratch_bytes) may be passed in; calls that overlap need their own."""
         M, H = self._rows(batch, q)
+        window = max(-2, min(int(window), _INT_MAX))  # beyond every length, or refused, all the same
         n_sel = 0
         if blocks is not None:
             n_sel = blocks.shape[-1]
@@ -196,7 +200,7 @@ class KVCache:
             scratch = self._tiles.new_empty(self.scratch_bytes(batch, M, H, n_sel))
         else:
             _check(scratch, "scratch", torch.uint8, self._device)
-        _launch("gpt_op_attention_kv", self._device, self._ref, batch._ref, q.data_ptr(), M, H, int(window),
+        _launch("gpt_op_attention_kv", self._device, self._ref, batch._ref, q.data_ptr(), M, H, window,
                 blocks.data_ptr() if blocks is not None else None, n_sel, o.data_ptr(), lse.data_ptr(),
                 scratch.data_ptr(), scratch.numel())
         return o, lse

@@ -975,3 +975,17 @@ def test_selection_leaves_the_rows_of_a_broken_sequence_as_they_are(lens, cu, ma
     assert blocks[0, :, 0].tolist() == [0, 0] and blocks[0, :, 2].tolist() == [3, 3] and not torch.any(scores[0] == 77.0)
     for m in good[1:]:
         assert blocks[m].tolist() == [[0, -1, -1]] * 2 and torch.all(scores[m, :, 1:] == -float("inf"))
+
+
+def test_a_window_beyond_32_bits_is_no_window():
+    """Python numbers are longer than the call's: a window of 2^40 must not become one of 0."""
+    w = World(8, 64, 2, [300, 70], 93)
+    batch, _ = w.batch([3, 2])
+    q = bf(normal((5, 256), 4))
+    o, lse = w.cache.attend(batch, q)
+    for window in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 3, 2 ** 40, 2 ** 63 - 1):
+        o2, lse2 = w.cache.attend(batch, q, window=window)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), window
+    for window in (-2, -2 ** 31, -2 ** 32, -2 ** 40):
+        with pytest.raises(_g().GptError):
+            w.cache.attend(batch, q, window=window)

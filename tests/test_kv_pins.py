@@ -213,3 +213,22 @@ def test_the_attributes_that_the_calls_go_by_cannot_be_assigned_to():
     b.lens.add_(1)
     assert lens.tolist() == [1, 2]
     assert g.KVBatch(b.block_table, b.lens).cu_new is None and g.KVCache(5, 2, 64, tiles=tiles, bounds=False).bounds is None
+
+
+def test_the_binding_refuses_numbers_that_32_bits_would_cut_off():
+    """2^32 + 1 chosen blocks must not become one, nor 2^40 first ones none."""
+    import torch
+
+    import decoder_only_gpt_tcgen05_b200 as g
+    table, lens, cu = torch.zeros((1, 1), dtype=torch.int32), torch.ones(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    c = g.KVCache(1, 1, 64, bits=8, tiles=torch.zeros((1, 1, g.kv.tile_bytes(8, 64)), dtype=torch.uint8))
+    b, q = g.KVBatch(table, lens), torch.zeros((1, 64), dtype=torch.bfloat16)
+    out = torch.zeros((1, 1, 1), dtype=torch.int32), torch.zeros((1, 1, 1))
+    for bad in (2 ** 31, 2 ** 32, 2 ** 40, 2 ** 63 - 1, -2 ** 40, float("inf")):
+        for name in ("n_first", "n_last"):
+            with pytest.raises(AssertionError, match="n_first"):
+                c.select(b, q, 1, **{name: bad}, blocks=out[0], scores=out[1])
+        with pytest.raises(AssertionError, match="max_new"):
+            g.KVBatch(table, lens, cu, max_new=bad)
+    with pytest.raises(AssertionError, match="n_select"):
+        c.select(b, q, 2 ** 32 + 1)
