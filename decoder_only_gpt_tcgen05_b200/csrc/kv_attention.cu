@@ -267,20 +267,46 @@ __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((unsigned
 constexpr int kAttendMaxWorkers = 160 * 16;
 constexpr int kScanSmem = 512;  // entries scanned by every CTA itself
 
-// Keys of a unit (U), ring depth and CTAs an SM.  A unit is one fetch: 64 keys, or 32 for 128-wide
-// 8-bit rows, whose 64 would leave room for too few warps.  The rings hold about 200 KB an SM, far above
+constexpr int kSmShared = 228 * 1024;  // of an SM
+constexpr int kAttendStages = 2;       // units of a warp's ring
+
+// What a CTA of W warps with tiles of RT query rows has in shared memory beside its rings.  What is the same
+// for a whole (entry, head), of the computing and the fetching iterator, lives here, written by lane 0, since
+// the registers are needed for the step.
+template <int W, int RT>
+struct __align__(128) AttendShared {
+  long long pre[kScanSmem + 1];
+  int cnt[kScanSmem + 1];
+  uint64_t bars[W][kAttendStages];
+  int meta[W][kAttendStages];  // of a stage's unit: first key; -1: none; -2 - first key: bad block
+  long long scan_units[W];
+  int scan_cnt[W];
+  KvEntry ent[W], fent[W];
+  KvSpan span[W];
+  int pos[W][RT];
+  long long row[W][RT];
+  int abort_flag;
+};
+
+// Keys of a unit (U) and CTAs an SM.  A unit is one fetch: 64 keys, or 32 for 128-wide
+// 8-bit rows, whose 64 would leave room for too few warps.  The rings hold 100 to 200 KB an SM, far above
 // the 44 KB that cover HBM's latency; 12 warps an SM leave each thread the 168 registers that one query
-// column tile needs, 8 warps the 255 of two.
+// column tile needs (and two of 64-wide rows), 8 warps the 255 of two; 16 warps fit with small rings only.
+// A CTA that does not fit runs after the others, with a full share of the work: 64 sequences of 2k to 8k
+// tokens, heads of 64: 8 bits, 12 kv heads 104 us with four CTAs launched an SM, of which three fit, 96 with
+// three; 4 bits, 16 query rows 46 us with three launched of four stages, of which two fit, 33 with two, 32
+// with three of two stages.
 template <class G, int NT>
 struct AttendCfg {
   static constexpr int U = G::REC > 8000 ? 32 : 64;
   static constexpr int WARPS = 4;
-  static constexpr int CTAS = (NT > 1 ? 2 : 3) + (G::HD == 64);
+  static constexpr int CTAS = NT > 1 ? (G::HD == 64 ? 3 : 2) : (G::HD == 64 && G::BITS == 4 ? 4 : 3);
   static constexpr int STAGE = U / kKvRec * G::REC;
-  static constexpr int FIT = 220 * 1024 / (WARPS * CTAS * STAGE);
-  static constexpr int STAGES = FIT < 4 ? 2 : 4;  // a power of two
+  static constexpr int STAGES = kAttendStages;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int SMEM = WARPS * RING;
+  // the rings, what else a CTA holds in shared memory, and 1 KB that the system takes of each
+  static_assert(CTAS * (SMEM + sizeof(AttendShared<WARPS, 8 * NT>) + 1024) <= kSmShared, "every CTA must be resident");
 };
 
 // NT tiles of 8 query columns.  A lane's part of a product's output is two neighbouring columns: QC = 1
@@ -299,19 +325,14 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   constexpr int U = C::U;  // keys of a unit
   constexpr int TL = NT == 2 ? (G::BITS == 8 && HD == 128 ? 2 : 1) : QC == 2 ? 2 : U / 16;  // 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
-  __shared__ uint64_t bars[C::WARPS][C::STAGES];
-  __shared__ int meta[C::WARPS][C::STAGES];  // of a stage's unit: first key; -1: none; -2 - first key: bad block
-  __shared__ long long s_pre[kScanSmem + 1];
-  __shared__ int s_cnt[kScanSmem + 1];
-  __shared__ long long s_warp[C::WARPS];
-  __shared__ int s_wcnt[C::WARPS];
-  // Of the computing and the fetching iterator: what is the same for a whole (entry, head) lives in
-  // shared memory, written by lane 0, since the registers are needed for the step.
-  __shared__ KvEntry s_ent[C::WARPS], s_fent[C::WARPS];
-  __shared__ KvSpan s_span[C::WARPS];
-  __shared__ int s_pos[C::WARPS][RT];
-  __shared__ long long s_row[C::WARPS][RT];
-  __shared__ int abort_flag;
+  __shared__ AttendShared<C::WARPS, 8 * NT> sh;
+  auto &bars = sh.bars;
+  auto &meta = sh.meta;
+  auto &s_ent = sh.ent, &s_fent = sh.fent;
+  auto &s_span = sh.span;
+  auto &s_pos = sh.pos;
+  auto &s_row = sh.row;
+  int& abort_flag = sh.abort_flag;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c = lane & 3;
   if (lane == 0) {
     for (int i = 0; i < C::STAGES; ++i) mbar_init(&bars[warp][i], 1);
@@ -325,9 +346,9 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   const long long* pre = p.prefix;
   const int* cnt = p.count;
   if (!p.scanned) {
-    pre = s_pre, cnt = s_cnt;
+    pre = sh.pre, cnt = sh.cnt;
     const bool first = blockIdx.x == 0;
-    kv_scan<SPARSE, C::WARPS>(p, RT, U, first, s_warp, s_wcnt, s_pre, s_cnt, first ? p.prefix : nullptr, p.count);
+    kv_scan<SPARSE, C::WARPS>(p, RT, U, first, sh.scan_units, sh.scan_cnt, sh.pre, sh.cnt, first ? p.prefix : nullptr, p.count);
   } else {
     __syncthreads();
   }
