@@ -989,3 +989,14 @@ def test_a_window_beyond_32_bits_is_no_window():
     for window in (-2, -2 ** 31, -2 ** 32, -2 ** 40):
         with pytest.raises(_g().GptError):
             w.cache.attend(batch, q, window=window)
+
+
+@pytest.mark.parametrize("case", [
+    (8, 128, 10, 10, True, True, [70, 130, 64, 7], [4, 5, 6, 7]),      # a token for each lane group of 128 dims
+    (4, 128, 8, 2, True, True, [66, 131, 3, 260], [7, 6, 3, 7]),       # in both blocks, in one, in none
+    (4, 64, 12, 12, True, False, [66, 131, 7], [7, 5, 4]),             # none of 64 dims
+    (8, 64, 9, 3, False, True, [66, 131, 8], [8, 7, 8]),
+])
+def test_append_of_a_few_drafted_tokens(case):
+    """New tokens about as many as a warp has lane groups, which decides how tokens and heads are dealt."""
+    test_append_and_read_match_the_oracle(case)
