@@ -29,7 +29,10 @@
 // Numbers: scores, maxima, sums and outputs are fp32; q is scaled by a power of two into fp16, which
 // is exact for a bf16 q down to 2^-28 of its row's largest; probabilities times the value scale are
 // rounded to fp16: by 2^-11 of their size at most (bf16's step would be eight times that), or, those below
-// 2^-19 of the largest value scale that the worker has met, by 2^-30 of that scale.
+// 2^-19 of the largest value scale that the row has met (in this worker's part of its keys), by 2^-30 of that
+// scale.  The unit that this goes by is each row's own: one for the tile would take 1 to 5 % off tiles of 16
+// rows, but a large value that a row may not see (a newer token's, or one that has left the window) would wipe out
+// that row.
 #include <cfloat>
 #include <cmath>
 #include <string>
@@ -439,7 +442,8 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   const int window = SPARSE ? -1 : p.window;
   unsigned int qb[NT][MT][2];
   float csum[NT][NG][4], qmul[NT][QC];  // accumulator start (-Z sum q), and q's scale times log2(e) / sqrt(hd)
-  float acc[NT][MT][2 * QC], m[NT][QC], l[NT][QC], vinv;  // vinv: 64 / (the values' unit), a power of two
+  // vinv: 64 / (the values' unit of the row), a power of two, at most 2^118; vinv_top: the rows' largest
+  float acc[NT][MT][2 * QC], m[NT][QC], l[NT][QC], vinv[NT][QC], vinv_top;
   auto begin = [&]() {
     const KvEntry t = s_ent[warp];
     if (lane == 0) {
@@ -511,13 +515,12 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
               __shfl_sync(0xffffffffu, sum[g], (2 * c + i) * 4) * (-G::Z * 5.9604644775390625e-8f);
       }
 #pragma unroll
-      for (int i = 0; i < QC; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f;
+      for (int i = 0; i < QC; ++i) m[nt][i] = -FLT_MAX, l[nt][i] = 0.f, vinv[nt][i] = vinv_top = exp2i(118);
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int k = 0; k < 2 * QC; ++k) acc[nt][i][k] = 0.f;
     }
-    vinv = exp2i(126);
   };
 
   // ---- end of one (entry, head) in this worker: the output, or this worker's part of it
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         const long long qrow = s_row[warp][n];
         if (qrow >= 0) {
           // acc is in units of 2^-24 / vinv; the rows of bits 4..7 in 16 times that
-          const float f = sum == 0.f ? 0.f : 16777216.f / sum, fi = 1.f / vinv;
+          const float f = sum == 0.f ? 0.f : 16777216.f / sum, fi = 1.f / vinv[nt][i];
           const float lse2 = sum == 0.f ? -INFINITY : m[nt][i] + log2f(sum);
 #pragma unroll
           for (int wj = 0; wj < HD / 64; ++wj) {
@@ -660,65 +663,75 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
             }
         }
       }
-      if (edge) {  // masked pairs get -inf; a key that no row of the tile sees also loses its value scale
+      // The running maximum may lag by 8 (a factor 256 in p), and the values' unit is a power of two at or
+      // above every scale that the row has seen: both move seldom, so the usual step costs one vote here.
+      float xm[NT][QC], vm[NT][QC];
+      auto pair = [&](int tl, int hf) { return *reinterpret_cast<const __nv_bfloat162*>(&vs[tl][hf]); };
+      if (edge) {  // masked pairs get -inf, and their scales do not count
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < QC; ++q) vm[nt][q] = 0.f;
 #pragma unroll
         for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int key = kb + tl * 16 + gid + 8 * hf;
-            if (key > p_hi || (window >= 0 && key < sp.p_lo - window)) vs[tl][hf] = 0;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int q = 0; q < QC; ++q) {
                 const int pos = s_pos[warp][QC == 1 ? c : nt * 8 + 2 * c + q];
                 if (key > pos || (window >= 0 && key < pos - window)) x[tl][nt][QC * hf + q] = -INFINITY;
+                else vm[nt][q] = fmaxf(vm[nt][q], fmaxf(bf16_lo(vs[tl][hf]), bf16_hi(vs[tl][hf])));
               }
           }
+      } else {
+        __nv_bfloat162 v2 = __hmax2(pair(0, 0), pair(0, 1));
+#pragma unroll
+        for (int tl = 1; tl < TL; ++tl) v2 = __hmax2(v2, __hmax2(pair(tl, 0), pair(tl, 1)));
+        const float v = fmaxf(__low2float(v2), __high2float(v2));
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int q = 0; q < QC; ++q) vm[nt][q] = v;
       }
-      // The running maximum may lag by 8 (a factor 256 in p), and the values' unit is a power of two
-      // at or above every scale seen: both move seldom, so the usual step costs one vote here.
-      float xm[NT][QC];
-      __nv_bfloat162 vm2 = *reinterpret_cast<const __nv_bfloat162*>(&vs[0][0]);
-#pragma unroll
-      for (int tl = 0; tl < TL; ++tl)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          vm2 = __hmax2(vm2, *reinterpret_cast<const __nv_bfloat162*>(&vs[tl][hf]));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int q = 0; q < QC; ++q)
-              xm[nt][q] = tl == 0 && hf == 0 ? x[0][nt][q] : fmaxf(xm[nt][q], x[tl][nt][QC * hf + q]);
-        }
-      float vm = fmaxf(__low2float(vm2), __high2float(vm2));
-      bool move = vm * vinv > 64.f;
+      bool move = false;
+      float vm_top = 0.f;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int q = 0; q < QC; ++q) move |= fmaf(xm[nt][q], qmul[nt][q], -m[nt][q]) > 8.f;
-      if (__any_sync(0xffffffffu, move)) {
+        for (int q = 0; q < QC; ++q) {
+          xm[nt][q] = x[0][nt][q];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, o));
-        float fv = 1.f;
-        if (vm * vinv > 64.f) {  // the unit becomes the power of two above vm
-          const float nv = exp2i(max(6 - ((int)(__float_as_uint(vm) >> 23) - 126), -121));
-          fv = nv / vinv;
-          vinv = nv;
+          for (int tl = 0; tl < TL; ++tl) xm[nt][q] = fmaxf(fmaxf(xm[nt][q], x[tl][nt][q]), x[tl][nt][QC + q]);
+          move |= fmaf(xm[nt][q], qmul[nt][q], -m[nt][q]) > 8.f;
+          vm_top = fmaxf(vm_top, vm[nt][q]);
         }
+      move |= vm_top * vinv_top > 64.f;
+      if (__any_sync(0xffffffffu, move)) {
+        vinv_top = 0.f;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[QC];
 #pragma unroll
           for (int q = 0; q < QC; ++q) {
-            float mx = xm[nt][q];
+            float mx = xm[nt][q], v = vm[nt][q];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            for (int o = 4; o < 32; o <<= 1) {
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            }
             mx = fmaxf(m[nt][q], mx * qmul[nt][q]);
             f[q] = m[nt][q] == mx ? 1.f : ex2_approx(m[nt][q] - mx);
             m[nt][q] = mx;
             l[nt][q] *= f[q];
-            f[q] *= fv;
+            if (v * vinv[nt][q] > 64.f) {  // the unit becomes the power of two above v
+              const float nv = exp2i(max(6 - ((int)(__float_as_uint(v) >> 23) - 126), -121));
+              f[q] *= nv / vinv[nt][q];
+              vinv[nt][q] = nv;
+            }
+            vinv_top = fmaxf(vinv_top, vinv[nt][q]);
           }
 #pragma unroll
           for (int y = 0; y < MT; ++y)
@@ -732,9 +745,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
       for (int tl = 0; tl < TL; ++tl)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          float sv[NG];
-          sv[0] = bf16_lo(vs[tl][hf]) * vinv;
-          if (NG == 2) sv[NG - 1] = bf16_hi(vs[tl][hf]) * vinv;
+          const float sc[2] = {bf16_lo(vs[tl][hf]), bf16_hi(vs[tl][hf])};  // (the second is 0 with one scale a row)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float pr[QC];
@@ -745,14 +756,15 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
             }
 #pragma unroll
             for (int g = 0; g < PG; ++g) {
-              float w[2] = {0.f, 0.f};
+              float w[2] = {0.f, 0.f};  // (pr vinv is at most 2^126)
               if (QC == 1) {
 #pragma unroll
-                for (int k = 0; k < NG; ++k) w[k] = edge && x[tl][nt][hf] == -INFINITY ? 0.f : pr[0] * sv[k];
+                for (int k = 0; k < NG; ++k)
+                  w[k] = edge && x[tl][nt][hf] == -INFINITY ? 0.f : pr[0] * vinv[nt][0] * sc[k];
               } else {
 #pragma unroll
                 for (int q = 0; q < QC; ++q)
-                  w[q] = edge && x[tl][nt][QC * hf + q] == -INFINITY ? 0.f : pr[q] * sv[g];
+                  w[q] = edge && x[tl][nt][QC * hf + q] == -INFINITY ? 0.f : pr[q] * vinv[nt][q] * sc[g];
               }
               pb[tl][g][nt][hf] = transpose8(pack_h2(w[0], w[1]));
             }

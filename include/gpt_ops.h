@@ -300,6 +300,10 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
  *        (may be NULL).  A row without keys gets o = 0 and lse = -inf.
  *   scratch  gpt_op_attention_kv_scratch_size bytes, 256-byte aligned; calls
  *        that may overlap need scratch of their own
+ * q counts as finite below 2^117 (a row with more gives NaN) and scores must
+ * stay within fp32.  Probability times value scale is rounded to fp16 (11 bits)
+ * in a unit of the row's own: what lies below 2^-19 of the largest value scale
+ * among the keys that the row sees is off by up to 2^-30 of that scale.
  * Results do not depend on timing, but the split of the keys (and with it the
  * last bits) depends on the whole batch. */
 GPT_API int gpt_op_attention_kv_scratch_size(const gpt_kv_cache* cache, const gpt_kv_batch* batch, int M, int H,

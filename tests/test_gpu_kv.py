@@ -1000,3 +1000,39 @@ def test_a_window_beyond_32_bits_is_no_window():
 def test_append_of_a_few_drafted_tokens(case):
     """New tokens about as many as a warp has lane groups, which decides how tokens and heads are dealt."""
     test_append_and_read_match_the_oracle(case)
+
+
+@pytest.mark.parametrize("bits,hd,H,Hkv,new,window", [
+    (8, 128, 2, 2, 4, -1), (4, 128, 2, 2, 2, -1), (8, 64, 12, 2, 1, 40),      # tiles of 4 and 8 rows
+    (8, 128, 2, 1, 4, -1), (4, 128, 4, 2, 3, -1), (4, 64, 4, 1, 2, -1), (8, 64, 6, 2, 2, 31),
+    (8, 128, 4, 1, 4, -1), (4, 128, 4, 1, 5, -1), (4, 64, 2, 2, 40, 20), (8, 64, 2, 1, 66, 64)])     # of 16
+@pytest.mark.parametrize("size", [2.0 ** 12, 2.0 ** 40, 1e30])
+def test_large_values_of_keys_that_a_row_does_not_see_leave_it_alone(bits, hd, H, Hkv, new, window, size):
+    """A value row of any finite size, in the place of a newer token's or of one that has left the window,
+    changes the rows that see it and no other: those stay within the tolerance of their own keys."""
+    L = 150 + new
+    for at in (L - 1, L - 1 - new // 2, L - 1 - new // 2 - max(window, 0)):      # the large value's position
+        w = World(bits, hd, Hkv, [L], 94)
+        R, ng, recb = O.kv.geometry(bits, hd)
+        rec, tok = divmod(at % 64, 32)
+        so = rec * recb + 2 * 32 * R + 64 * ng + tok * 2 * ng
+        dst = w.cache.tiles[w.table[0, at // 64]][:, so:so + 2 * ng].clone().view(torch.bfloat16)
+        w.cache.tiles[w.table[0, at // 64], :, so:so + 2 * ng] = (dst.float() * size).bfloat16().view(torch.uint8)
+        q = bf(normal((new, H * hd), 4))
+        o, lse = w.cache.attend(w.batch([new])[0], q, window=window)
+        _g().model.sync_status(DEV)
+        blind = 0
+        for m in range(new):
+            p = L - new + m
+            lo = max(0, p - window) if window >= 0 else 0
+            if lo <= at <= p:
+                continue
+            blind += 1
+            wt = np.zeros((Hkv, L))
+            wt[:, lo:p + 1] = 1.0
+            qr = f64(q)[m].reshape(H, hd)
+            ro, rl, av = O.kv.attend(qr, w.k[0], w.v[0], wt)
+            to, tl = attend_bounds(w, 0, qr, ro, rl, av, wt)
+            assert np.all(np.abs(f64(o)[m].reshape(H, hd) - ro) <= to), (at, m)
+            assert np.all(np.abs(f64(lse)[m] - rl) <= tl), (at, m)
+        assert blind > 0 or new == 1 or at == L - new
