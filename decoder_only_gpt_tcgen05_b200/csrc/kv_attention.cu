@@ -1029,7 +1029,7 @@ static int attend_plan(const char* what, const gpt_kv_cache* c, const gpt_kv_bat
   const long long qt = rows > 0 ? (rows + p.RT - 1) / p.RT : 0;
   p.RV = (int)(rows < p.RT ? (rows > 0 ? rows : 1) : p.RT);
   p.E = (sparse ? (long long)M : (long long)b->n_seq) * qt;
-  if (qt > 0x7fffffffLL || p.E * c->n_kv_head * p.RV > 0x7fffffffLL)
+  if (qt > 0x7fffffffLL || p.E > 0x7fffffffLL / ((long long)c->n_kv_head * p.RV))  // (the product may pass 2^63)
     return set_error(ST_UNSUPPORTED, w + ": too many query rows");
   p.QT = (int)qt;
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };

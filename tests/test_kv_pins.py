@@ -232,3 +232,17 @@ def test_the_binding_refuses_numbers_that_32_bits_would_cut_off():
             g.KVBatch(table, lens, cu, max_new=bad)
     with pytest.raises(AssertionError, match="n_select"):
         c.select(b, q, 2 ** 32 + 1)
+
+
+@pytest.mark.parametrize("n_seq,max_new,H,Hkv,n_sel", [
+    (2 ** 31 - 1, 2 ** 31 - 1, 64, 64, 0),        # products that pass 2^63, and come out below the limit
+    (2 ** 31 - 1, 2 ** 31 - 16, 128, 128, 0), (2 ** 31 - 1, 5, 64, 64, 0), (3, 5, 2 ** 30, 2 ** 29, 9),
+    (1, 2 ** 31 - 1, 2 ** 30, 1, 0)])
+def test_a_batch_of_too_many_rows_is_refused_whatever_its_products_come_to(n_seq, max_new, H, Hkv, n_sel):
+    import decoder_only_gpt_tcgen05_b200 as g
+    L = g.lib()
+    c, b = _args(dict(n_kv_head=Hkv), dict(n_seq=n_seq, max_new=max_new, max_blocks=1))
+    n = C.c_size_t()
+    M = 2 ** 31 - 1
+    assert L.gpt_op_attention_kv_scratch_size(c, b, M, H, n_sel, C.byref(n)) == 2
+    assert L.gpt_op_attention_kv(c, b, P, M, H, -1, P if n_sel else None, n_sel, P, P, P, 0, None) == 2
