@@ -23,11 +23,13 @@
 //     joined, in order, by kv_join_kernel, so results do not depend on timing.
 //
 // Measured (20-layer model's 10 heads of 128, replayed from a graph): 32 sequences of 16k to 32k tokens in 4
-// bits 178 us, 6.0 TB/s; 64 of 65 to 2048 in 8 bits 43 us, 4.1 TB/s, of which 30 us at 6.0 and the rest start,
-// join and launches; one of 2047 in 4 bits 8.9 us, all of it latency.
+// bits 176 us, 6.1 TB/s; 64 of 65 to 2048 in 8 bits 41.4 us, 4.3 TB/s, of which 28 us are bytes and the rest start,
+// join and launches; one of 2047 in 4 bits 8.3 us, all of it latency.  Several new tokens: a tile of 16 query rows
+// reads and unpacks the cache once, so a chunk of n tokens of a head takes n / 16 passes over its keys (16 prompts
+// of 2048 tokens 1200 us, where gpt_op_attention_fwd takes 376 for the same rows without a cache).
 //
 // Numbers: scores, maxima, sums and outputs are fp32; q is scaled by a power of two into fp16, which
-// is exact for a bf16 q down to 2^-28 of its row's largest; probabilities times the value scale are
+// is exact for a bf16 q down to 2^-27 of its row's largest (8 bits: 2^-31); probabilities times the value scale are
 // rounded to fp16: by 2^-11 of their size at most (bf16's step would be eight times that), or, those below
 // 2^-19 of the largest value scale that the row has met (in this worker's part of its keys), by 2^-30 of that
 // scale.  The unit that this goes by is each row's own: one for the tile would take 1 to 5 % off tiles of 16
@@ -268,7 +270,9 @@ __device__ __forceinline__ unsigned int lds2(uint32_t a) {
 __device__ __forceinline__ float exp2i(int e) { return __uint_as_float((unsigned int)(e + 127) << 23); }  // -126..127
 
 constexpr int kAttendMaxWorkers = 160 * 16;
-constexpr int kScanSmem = 512;  // entries scanned by every CTA itself
+// Entries scanned by every CTA itself; more have a launch of their own (8 bits, 2 heads: 64 sequences 18.6 us
+// against 19.9 with that launch, 256 20.1 against 21.0, 500 30.6 against 30.2).
+constexpr int kScanSmem = 512;
 
 constexpr int kSmShared = 228 * 1024;  // of an SM
 constexpr int kAttendStages = 2;       // units of a warp's ring
@@ -317,8 +321,9 @@ struct AttendCfg {
 // heads has one), and leaves out half of the softmax's and the output's arithmetic and registers.  A
 // step then takes a whole unit (TL tiles), a record with all columns, half of one with two column tiles:
 // what fits the registers (8 bits at 128 dims have one scale a row, which leaves room for a record: 16
-// prompts of 128 tokens 92.8 -> 89.1 us; at 64 dims it spills).  (32 sequences of 16k to 32k tokens in 4
-// bits: 212 us with both columns and a record a step, 198 with one, 185 with one and 64 keys a step.)
+// chunks of 512 tokens over 2k to 8k 1164 us, with half of one 1232; at 64 dims it spills).  (32 sequences of 16k to 32k tokens in 4
+// bits: 212 us with both columns and a record a step, 198 with one, 185 with one and 64 keys a step, when that was
+// built.)
 template <class G, int NT, int QC, bool SPARSE>
 __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>::CTAS) kv_attend_kernel(AttendArgs p) {
   using C = AttendCfg<G, NT>;
@@ -1064,7 +1069,10 @@ static int launch_attend(AttendArgs a, const AttendPlan& pl, double bytes, doubl
     Prof prof(PK_ATTN_FWD, flops, bytes, st);
     GPTK_CUDA(launch_pdl(kern, dim3(grid), dim3(C::WARPS * 32), C::SMEM, st, a));
   }
-  // warps a row of the join: by the parts that a row has on average when every worker is busy
+  // warps a row of the join: by the parts that a row has on average when every worker is busy (with eight, two
+  // and one; 8 bits, lengths to 4096: 4 x 10 heads, 44 parts, 13.1 / 16.0 / 19.4 us; 24 x 2 heads of 16 rows, 25 parts,
+  // 21.9 / 25.3 / 29.2; 48 of them, 12 parts, 32.1 / 30.2 / 32.5; 80, 7 parts, 46 / 39.9 / 41; 32 x 10 heads of one row,
+  // 5.5 parts, 57 / 57 / 53)
   const long long segs = pl.E * a.Hkv, workers = (long long)grid * C::WARPS;
   const long long parts = workers / segs;
   const int rows = (int)(segs * pl.RV);

@@ -16,8 +16,10 @@ namespace gptk {
 // its own.  The warp's 32 / (HD / 16) lane groups take tokens of one head, and the elementwise
 // bounds of the block's keys are carried in registers and joined across the groups at the end; a
 // block with fewer new tokens than groups (a decoding step) gives each group a head of its own.
-// Bounded by instruction issue: 18.5k tokens of 30 heads of 128 in 4 bits take 58 us, 3.7 TB/s, at 0.61
-// instructions a clock and scheduler (a third CTA an SM would spill: 70 us); a step of 16 tokens 3 us.
+// Bounded by latency with four warps a scheduler: 18.5k tokens of 30 heads of 128 in 4 bits take 58 us (33 of
+// bytes), 3.7 TB/s, at 0.61 instructions a clock and scheduler; for each, a warp waits 1.35 issue slots for its own
+// results and 0.9 for shared memory, the ring's and the tables' (a third CTA an SM would spill: 70 us).  A step of 16
+// tokens takes 3 us.
 struct RopeFreq {
   double f[64];  // base^(-2 i / hd)
 };
@@ -37,7 +39,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 // Eight values of one scale group to codes.  x / s is the product with an approximate reciprocal plus
-// its residual once more, which is the correctly rounded quotient: bf16 values over a bf16 scale often
+// its residual once more (Markstein's correction of an approximate quotient by fused multiply-adds, 1990), which
+// is exact where fp32 holds the quotient: bf16 values over a bf16 scale often
 // lie exactly between two codes, and the bare product would round those either way.  Adding 1.5 2^23 + Z
 // rounds it to the integer code in the sum's low bits (one fp32 add; a float-to-int conversion has an
 // eighth of its rate).  |x / s| <= top (1 + 2^-8) rounds to at most top, so nothing is clamped.
@@ -264,7 +267,7 @@ __device__ __forceinline__ void append_head(AppendCta& a_, int h, bool in_range)
       for (int g = 0; g < G::NG; ++g) {
         const float m = g ? mc : ma;
         constexpr float RT = 1.f / G::TOP;
-        const float q = m * RT;  // and its residual: m / TOP correctly rounded
+        const float q = m * RT;  // and its residual, as in encode8: m / TOP correctly rounded
         float v = __bfloat162float(__float2bfloat16_rn(fmaf(fmaf(-q, (float)G::TOP, m), RT, q)));
         if (v < FLT_MIN) v = 0.f;
         if (!(m < INFINITY)) v = __uint_as_float(0x7fc00000u);
@@ -612,9 +615,11 @@ GPT_API int gpt_op_kv_append(const gpt_kv_cache* cache, const gpt_kv_batch* batc
   Prof prof(PK_QK, 0, M * row * 2 + (double)M * H * cache->head_dim * 2, st);
   return kv_dispatch(cache, [&](auto g) -> int {
     using G = decltype(g);
-    // the heads are shared among enough CTAs to give every SM a few: turns of a warp, one for each head where
-    // a block can have a token for each of the SG lane groups, else one for SG heads (16 x 6 new tokens of 30
-    // heads of 128: 5.0 us, and 9.0 with a quarter of the CTAs)
+    // the heads are shared among enough CTAs to give every SM four (with one, two, four and eight, 30 heads of 128:
+    // 16 x 300 tokens 28.0 / 21.2 / 21.2 / 21.2 us, 64 x 300 53.8 / 53.8 / 52.7 / 50.1, 4 x 2048 28.4 / 23.0 / 21.5 / 21.5,
+    // 16 x 2048 54.3 / 54.4 / 56.7 / 60.7), as far as the warps have turns: one for each head where a block can have a
+    // token for each of the SG lane groups, else one for SG heads (16 x 6 new tokens 5.0 us, 9.0 with a quarter of
+    // the CTAs)
     constexpr int SG = 512 / G::HD;
     const long long ctas = bps * batch->n_seq;
     const int hw = max_new >= SG ? H + 2 * Hkv : (H + 2 * Hkv + SG - 1) / SG;

@@ -9,9 +9,12 @@
 // the choice hangs on comparisons of near scores, and a sum in fp32 would let the order of the
 // additions decide.  Equal scores go to the lower index.
 //
-// Measured, scores and choice together: 7 us for one sequence of 8k tokens (12 heads of 64: two launches and
-// four dependent loads), 13.7 us for 16 of 4k to 32k (10 heads of 128, 23 MB of bounds), 18.5 us for 64 rows of 16 heads
-// over 2 kv heads, where the fp64 conversions and products weigh.
+// Measured, scores and choice together: 7.0 us for one sequence of 8k tokens (12 heads of 64: two launches and
+// four dependent loads), 13.9 us for 16 of 4k to 32k (10 heads of 128, 23 MB of bounds), 18.5 us for 64 rows of 16
+// heads over 2 kv heads.  Alone and with a cold cache the scores take 5.8, 12.5 and 16.7 us, the choice 6.2, 7.5 and 6.2.
+// The grouped scores are bound by the conversions to fp64 (their pipe is busy for 52 % of the time, the fp64 products'
+// for 13 %) and by rows of uneven length (0.26 to 0.82 instructions a clock and scheduler, by SM); the choice by its
+// barriers (0.15 instructions a clock and scheduler).
 #include <string>
 
 #include "kv.cuh"

@@ -4,7 +4,8 @@ calls that take it) on torch tensors.
 ``KVCache`` bundles a layer's cache buffers; ``KVBatch`` describes the sequences of a call and their
 new tokens and is shared by all layers.  A step of a layer is ``append`` (RoPE, QK-norm, quantise),
 then ``attend``, over everything or over the blocks that ``select`` chose.  Nothing is read back to
-the host, so a step can be captured into a CUDA graph and replayed with new contents."""
+the host, so a step can be captured into a CUDA graph and replayed with new contents.  Rows that belong
+to no sequence are left as they are: in an output that a call makes itself they hold anything."""
 from __future__ import annotations
 
 import ctypes as C
@@ -186,6 +187,8 @@ class KVCache:
         """(o bf16 [M, n_head head_dim], lse fp32 [M, n_head]): attention of the new tokens over the cache,
         over all earlier keys, over the last ``window`` and itself, or over the listed ``blocks`` (of each
         list the first min(length, visible blocks) entries are read: put the visible ones first).
+        Made for a few new tokens a sequence: long chunks among single tokens are faster as a call of their own,
+        prompts without earlier keys as ops.attention_fwd.
         ``scratch`` (uint8, scratch_bytes) may be passed in; calls that overlap need their own."""
         M, H = self._rows(batch, q)
         window = max(-2, min(int(window), _INT_MAX))  # beyond every length, or refused, all the same

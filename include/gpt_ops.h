@@ -255,7 +255,7 @@ GPT_API int gpt_kv_tile_bytes(int bits, int head_dim, size_t* bytes);
  *   q_out  bf16 [M, H hd]: q after RoPE (if rope) and RMSNorm (if qk_norm)
  * Per scale group, with top = 7 or 127: scale = bf16(max|x| / top),
  * code - Z = round(x / scale) clamped to [-top, top] (k is not rounded to bf16
- * in between).  A group that holds an infinity or a NaN reads back as NaN; one
+ * in between; the norms' sums of squares are fp32, as there).  A group that holds an infinity or a NaN reads back as NaN; one
  * whose scale would be below 2^-126, as zeros.  Angles are formed in fp64.
  * With bounds, those of every touched block become the outward rounded
  * elementwise minimum and maximum of the values its keys now stand for; a
@@ -300,6 +300,11 @@ GPT_API int gpt_op_kv_select(const gpt_kv_cache* cache, const gpt_kv_batch* batc
  *        (may be NULL).  A row without keys gets o = 0 and lse = -inf.
  *   scratch  gpt_op_attention_kv_scratch_size bytes, 256-byte aligned; calls
  *        that may overlap need scratch of their own
+ * Made for a few new tokens a sequence: every 16 query rows of a kv head read
+ * their keys anew, and max_new decides for the whole batch how wide the tiles
+ * are and how many there are, whether sequences fill them or not.  A batch that
+ * mixes long chunks with single tokens is faster as two calls; a prompt without
+ * earlier keys as gpt_op_attention_fwd.
  * q counts as finite below 2^117 (a row with more gives NaN) and scores must
  * stay within fp32.  Probability times value scale is rounded to fp16 (11 bits)
  * in a unit of the row's own: what lies below 2^-19 of the largest value scale
