@@ -23,7 +23,7 @@
 //     joined, in order, by kv_join_kernel, so results do not depend on timing.
 //
 // Measured (20-layer model's 10 heads of 128, replayed from a graph): 32 sequences of 16k to 32k tokens in 4
-// bits 176 us, 6.1 TB/s; 64 of 65 to 2048 in 8 bits 41.4 us, 4.3 TB/s, of which 28 us are bytes and the rest start,
+// bits 178 us, 6.0 TB/s; 64 of 65 to 2048 in 8 bits 41.4 us, 4.3 TB/s, of which 28 us are bytes and the rest start,
 // join and launches; one of 2047 in 4 bits 8.3 us, all of it latency.  Several new tokens: a tile of 16 query rows
 // reads and unpacks the cache once, so a chunk of n tokens of a head takes n / 16 passes over its keys (16 prompts
 // of 2048 tokens 1200 us, where gpt_op_attention_fwd takes 376 for the same rows without a cache).
@@ -331,6 +331,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   // with one column used, a column pair's other half carries the weights of the second scale group
   constexpr int PG = QC == 1 ? 1 : NG;  // operands P a key tile
   constexpr int U = C::U;  // keys of a unit
+  constexpr bool IN_KS = NG <= NT * QC;  // where the scores' constant factor goes
   constexpr int TL = NT == 2 ? (G::BITS == 8 && HD == 128 ? 2 : 1) : QC == 2 ? 2 : U / 16;  // 16-key tiles of a step
   extern __shared__ __align__(128) uint8_t ring_all[];
   __shared__ AttendShared<C::WARPS, 8 * NT> sh;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
   // ---- state of one (entry, head)
   const int window = SPARSE ? -1 : p.window;
   unsigned int qb[NT][MT][2];
-  float csum[NT][NG][4], qmul[NT][QC];  // accumulator start (-Z sum q), and q's scale times log2(e) / sqrt(hd)
+  float csum[NT][NG][4], qmul[NT][QC];  // accumulator start (-Z sum q), and q's scale, a power of two
   // vinv: 64 / (the values' unit of the row), a power of two, at most 2^118; vinv_top: the rows' largest
   float acc[NT][MT][2 * QC], m[NT][QC], l[NT][QC], vinv[NT][QC], vinv_top;
   auto begin = [&]() {
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
         const float2 u = unpack_h2(b[0]), v = unpack_h2(b[1]);
         sum[g] += (u.x + u.y) + (G::BITS == 4 ? 16.f : 1.f) * (v.x + v.y);
       }
-      const float mul = odd ? __uint_as_float(0x7fc00000u) : p.scale_log2 * exp2i(ex + 10);
+      const float mul = odd ? __uint_as_float(0x7fc00000u) : exp2i(ex + 10);
 #pragma unroll
       for (int i = 0; i < QC; ++i) qmul[nt][i] = __shfl_sync(0xffffffffu, mul, (2 * c + i) * 4);
 #pragma unroll
@@ -611,7 +612,10 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
       const uint32_t saddr = rec + G::KSCALE + tile0 * 16 * 2 * NG + gid * 2 * NG;
       const uint32_t va = rec + G::VCODES + tile0 * 16 * G::ROWB + lane * 16;
       const bool edge = kb + 16 * TL - 1 > sp.p_lo || (window >= 0 && kb < p_hi - window);
-      // scores S^T[key][query], unscaled, and the value scales of the keys of this lane's rows
+      // scores S^T[key][query] but for q's scale, and the value scales of the keys of this lane's rows.  The factor
+      // log2(e) / sqrt(hd) goes into the key's scales, or, where that is less to multiply, into the score; what is
+      // left is a power of two, so the largest score is the maximum to the last bit (rounded apart from it, scores
+      // beyond 2^31 gave p = 2^256)
       float x[TL][NT][2 * QC];
       unsigned int vs[TL][2];
 #pragma unroll
@@ -658,13 +662,17 @@ __global__ void __launch_bounds__(AttendCfg<G, NT>::WARPS * 32, AttendCfg<G, NT>
             ks[0] = bf16_bits(lds2(sa));
             vs[tl][hf] = lds2(sa + G::VSCALE - G::KSCALE);
           }
+          if (IN_KS) {
+#pragma unroll
+            for (int g = 0; g < NG; ++g) ks[g] *= p.scale_log2;
+          }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int q = 0; q < QC; ++q) {
               float v = sc[0][nt][2 * hf + q] * ks[0];
               if (NG == 2) v = fmaf(sc[NG - 1][nt][2 * hf + q], ks[NG - 1], v);
-              x[tl][nt][QC * hf + q] = v;
+              x[tl][nt][QC * hf + q] = IN_KS ? v : v * p.scale_log2;
             }
         }
       }

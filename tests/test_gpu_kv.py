@@ -1036,3 +1036,48 @@ def test_large_values_of_keys_that_a_row_does_not_see_leave_it_alone(bits, hd, H
             assert np.all(np.abs(f64(o)[m].reshape(H, hd) - ro) <= to), (at, m)
             assert np.all(np.abs(f64(lse)[m] - rl) <= tl), (at, m)
         assert blind > 0 or new == 1 or at == L - new
+
+
+@pytest.mark.parametrize("bits,hd,H,Hkv,new", [
+    (8, 128, 2, 2, 1), (4, 128, 2, 2, 1), (4, 64, 3, 3, 1), (4, 128, 8, 1, 1), (8, 64, 4, 2, 3), (8, 128, 2, 2, 9),
+    (4, 128, 4, 1, 5)])
+@pytest.mark.parametrize("size", [1e3, 1e6, 1e9, 1e13, 1e25, 1e35])
+def test_scores_of_any_finite_size_choose_the_largest(bits, hd, H, Hkv, new, size):
+    """Scores far apart: the softmax is the largest one's value row and the logsumexp that score.  Looked at are
+    the rows where the first is ahead by 50 (e^-50 of the rest) and by 2^-6 of itself, which is above what the
+    scores can be off: 2^-11 of the largest |q| times a key's scale for 16 dims each."""
+    w = World(bits, hd, Hkv, [130 + new, 40], 95, scale=size ** 0.5)
+    w.v = [v / size ** 0.5 for v in w.v]
+    R, ng, recb = O.kv.geometry(bits, hd)
+    for b, n in enumerate(w.lens):
+        _, vs, w.v[b] = O.kv.quantise(w.v[b], bits)
+        vc, vs, _ = O.kv.quantise(w.v[b], bits)
+        for j in range((n + 63) // 64):
+            m = min(64, n - 64 * j)
+            part = [np.zeros((Hkv, 64, hd), np.uint8), np.full((Hkv, 64, ng), np.nan)]
+            part[0][:, :m], part[1][:, :m] = vc[64 * j:64 * j + m].transpose(1, 0, 2), vs[64 * j:64 * j + m].transpose(1, 0, 2)
+            new_t = O.kv.pack(np.zeros_like(part[0]), np.full_like(part[1], np.nan), *part, bits).reshape(Hkv, 2, recb)
+            old = w.cache.tiles[w.table[b, j]].view(Hkv, 2, recb)
+            t = torch.from_numpy(new_t).to(DEV)
+            old[:, :, 32 * R:64 * R] = t[:, :, 32 * R:64 * R]
+            old[:, :, 64 * R + 64 * ng:] = t[:, :, 64 * R + 64 * ng:]
+    batch, cu = w.batch([new, 1])
+    q = bf(normal((new + 1, H * hd), 4) * size ** 0.5)
+    o, lse = (f64(t) for t in w.cache.attend(batch, q))
+    _g().model.sync_status(DEV)
+    assert np.all(np.isfinite(o)) and np.all(np.isfinite(lse))
+    seen = 0
+    for b, n in enumerate((new, 1)):
+        for i in range(n):
+            m, L = cu[b] + i, w.lens[b] - n + i + 1
+            for h in range(H):
+                s = w.k[b][:L, h // (H // Hkv)] @ f64(q)[m].reshape(H, hd)[h] / np.sqrt(hd)
+                a = np.argsort(s)
+                if s[a[-1]] - s[a[-2]] < max(50.0, 2.0 ** -6 * np.abs(s).max()):
+                    continue
+                seen += 1
+                v = w.v[b][a[-1], h // (H // Hkv)]
+                got = o[m].reshape(H, hd)[h]
+                assert np.all(np.abs(got - v) <= 2.0 ** -8 * np.abs(v) + 2.0 ** -11 * np.abs(v).max()), (b, i, h)
+                assert abs(lse[m, h] - s[a[-1]]) <= 2.0 ** -8 * np.abs(s).max(), (b, i, h)
+    assert seen > 0 or size < 1e6
