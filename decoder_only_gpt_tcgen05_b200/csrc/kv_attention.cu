@@ -34,7 +34,10 @@
 // 2^-19 of the largest value scale that the row has met (in this worker's part of its keys), by 2^-30 of that
 // scale.  The unit that this goes by is each row's own: one for the tile would take 1 to 5 % off tiles of 16
 // rows, but a large value that a row may not see (a newer token's, or one that has left the window) would wipe out
-// that row.
+// that row.  The tensor cores align the terms of a product of 16 by their operands' exponents, of which a subnormal's
+// counts as 2^-14: what lies below 2^-15 of the largest weight (or |q|) of the 16, times one code step, is cut off.
+// Products are exact for weights down to 2^-5 and q down to 2^-8 of that largest; a result is off by at most 2^-11 of a
+// code step per unit of weight, which shows where a dominant key's value is near zero.
 #include <cfloat>
 #include <cmath>
 #include <string>

@@ -1081,3 +1081,53 @@ def test_scores_of_any_finite_size_choose_the_largest(bits, hd, H, Hkv, new, siz
                 assert np.all(np.abs(got - v) <= 2.0 ** -8 * np.abs(v) + 2.0 ** -11 * np.abs(v).max()), (b, i, h)
                 assert abs(lse[m, h] - s[a[-1]]) <= 2.0 ** -8 * np.abs(s).max(), (b, i, h)
     assert seen > 0 or size < 1e6
+
+
+@pytest.mark.parametrize("bits,hd,H,Hkv,new", [(8, 128, 2, 2, 1), (4, 128, 2, 2, 1), (4, 64, 6, 2, 2), (8, 64, 4, 1, 4),
+                                               (4, 128, 5, 1, 3)])
+def test_small_values_beside_a_dominant_key(bits, hd, H, Hkv, new):
+    """A key with most of the weight and nearly all of its value zero: what the others leave is small next to
+    the terms that are summed.  A product of 16 cuts each term off below 2^-15 of its largest weight times a code
+    step (a subnormal operand's exponent counts as 2^-14, its mantissa has 10 bits), so a row is off by up to
+    16 x 2^-15 = 2^-11 of sum_j p_j scale_j beside the other roundings, and a score by as much of the largest |q|
+    times the key's scale for each 16 dims."""
+    L = 100 + new
+    w = World(bits, hd, Hkv, [L], 96)
+    xk, xv = w.k[0].copy(), normal((L, Hkv, hd), 97)
+    qv = normal((new, Hkv, H // Hkv, hd), 98)
+    for i in range(new):
+        for h in range(Hkv):
+            qm = qv[i, h].mean(0)
+            xk[5 + 20 * i, h] = 8 * np.sqrt(hd) * qm / (qm @ qm)      # a score of 8 on average
+            xv[5 + 20 * i, h, 1:] = 0.0
+            xv[5 + 20 * i, h, 0] = 3.0
+    kc, ks, w.k[0] = O.kv.quantise(xk, bits)
+    vc, vs, w.v[0] = O.kv.quantise(xv, bits)
+    for j in range((L + 63) // 64):
+        part = []
+        for a in (kc, ks, vc, vs):
+            t = np.zeros((Hkv, 64, a.shape[-1]), a.dtype)
+            m = min(64, L - 64 * j)
+            t[:, :m] = a[64 * j:64 * j + m].transpose(1, 0, 2)
+            part.append(t)
+        w.cache.tiles[w.table[0, j]] = torch.from_numpy(O.kv.pack(*part, bits)).to(DEV)
+    batch, _ = w.batch([new])
+    q = bf(qv.reshape(new, H * hd))
+    o, lse = (f64(t) for t in w.cache.attend(batch, q))
+    _g().model.sync_status(DEV)
+    G, Z = H // Hkv, 1 << (bits - 1)
+    top = 0.0
+    for i in range(new):
+        n = L - new + i + 1
+        qr = f64(q)[i].reshape(H, hd)
+        ro, rl, av = O.kv.attend(qr, w.k[0][:n], w.v[0][:n], np.ones((Hkv, n)))
+        for h in range(H):
+            ksc, vsc = (np.abs(x[:n, h // G]).max(-1) / (Z - 1) * (1 + 2.0 ** -7) for x in (w.k[0], w.v[0]))
+            p = np.exp(w.k[0][:n, h // G] @ qr[h] / np.sqrt(hd) - rl[h])
+            top = max(top, p.max())
+            es = (2.0 ** -20 * np.abs(qr[h]).sum() * 2 * Z + 2.0 ** -11 * hd / 16 * np.abs(qr[h]).max()) * ksc.max() / np.sqrt(hd)
+            to = 2.0 ** -8 * np.abs(ro[h]) + (2.0 ** -11 + 2 * es) * av[h] + 2.0 ** -11 * (p * vsc).sum() + \
+                2.0 ** -20 * 2 * Z * (p * vsc).sum()
+            assert np.all(np.abs(o[i].reshape(H, hd)[h] - ro[h]) <= to * (1 + 2.0 ** -6)), (i, h)
+            assert abs(lse[i, h] - rl[h]) <= es + 2.0 ** -21 * (1 + abs(rl[h])), (i, h)
+    assert top > 0.9
