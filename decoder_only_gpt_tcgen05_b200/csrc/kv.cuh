@@ -95,7 +95,7 @@ __device__ __forceinline__ void kv_report_bad(const KvRows& r, const DevCtl& ctl
 }
 
 // The sequence that row m belongs to and the row's position, by a whole block at once (one round of
-// loads), which must have no other barrier under way; b = -1 for a row of no sequence, or of one out of
+// loads; every thread calls this, once a kernel); b = -1 for a row of no sequence, or of one out of
 // range.  Both numbers are one 64-bit word, so that a row that two sequences claim gets one sequence's.
 struct KvRow {
   int b, pos;
